@@ -298,6 +298,135 @@ msr_status msr_layer_decode_step_noalloc(msr_dtype dtype, int32_t batch, int32_t
                                          const void* W_O, float* S, void* out, void* stream);
 size_t msr_layer_decode_noalloc_max_bytes(void);
 
+/* ---- Training between retention cores ------------------------------------
+ * What a block does between two retention cores, forward and backward, and
+ * activations kept in 8 bits from the one to the other ([RN-zh] sections
+ * "門控多尺度 Retention" and "Retention 網路總體結構": the per-head GroupNorm
+ * with the swish gate, the LayerNorms and the residual connections).
+ * Tensors, weights, biases, scales and workspaces are contiguous and 16-byte
+ * aligned (else MSR_ERR_UNSUPPORTED); vectors (these, statistics, gradients
+ * summed over tokens) are float32.  Norms, sums and gates are formed in float32 and rounded once;
+ * sums over tokens are added in a fixed order (the same bits every time).
+ *
+ * 8-bit form (fmt MSR_Q_E4M3 or MSR_Q_I8) of a tensor whose last dimension
+ * is a multiple of 32: 32 neighbouring values share a power of two 2^e, the
+ * smallest (e >= -127) with max|x| <= 448 * 2^e or 127 * 2^e.  *_q holds
+ * one byte a value, x * 2^-e rounded to nearest even as e4m3 or int8; *_qs
+ * one byte a group, e + 127.  A group with an infinity or a NaN gets 255
+ * and reads back as NaN.  q * 2^e is exact in bf16 and float32 (down to the
+ * type's smallest subnormal; magnitudes past 1.9375 * 2^127 round to infinity
+ * in e4m3).  MSR_Q_NONE: the tensor itself, in dtype. */
+typedef enum {
+  MSR_Q_NONE = 0,
+  MSR_Q_E4M3 = 1,
+  MSR_Q_I8 = 2,
+  MSR_Q_RANGE_MIN_ = -2147483647 - 1,
+  MSR_Q_RANGE_MAX_ = 2147483647
+} msr_qfmt;
+
+/* MSR_NORM_LAYER: centred, biased variance (LayerNorm; per head, GroupNorm).
+ * MSR_NORM_RMS: not centred, mean square (no mean is read or written). */
+typedef enum {
+  MSR_NORM_LAYER = 0,
+  MSR_NORM_RMS = 1,
+  MSR_NORM_RANGE_MIN_ = -2147483647 - 1,
+  MSR_NORM_RANGE_MAX_ = 2147483647
+} msr_norm;
+
+/* Residual sum and the norm before the next block, per row of d:
+ *   h = rn(alpha x + scale (.) b)     (rn: rounded to dtype)
+ *   mu = mean(h) (MSR_NORM_RMS: 0),  r = 1 / sqrt(mean((h - mu)^2) + eps)
+ *   y = (h - mu) r (.) weight + bias
+ * X, B, H, Y: [rows, d] (dtype).  B may be NULL: h = rn(alpha x).  scale,
+ * weight, bias: [d], NULL: 1, 1, 0.  H (the new residual stream) may be NULL:
+ * not written.  mean, rstd: [rows], may be NULL; the backward needs rstd, and
+ * mean for MSR_NORM_LAYER.  With fmt != MSR_Q_NONE, h is also kept in 8 bits
+ * in H_q, H_qs, and B in B_q, B_qs unless both are NULL (dscale needs it).
+ * d a multiple of 64, at most 8192; eps >= 0.  No workspace. */
+msr_status msr_resid_norm_fwd(msr_dtype dtype, msr_norm norm, int32_t rows, int32_t d,
+                              float alpha, float eps, const void* X, const void* B,
+                              const float* scale, const float* weight, const float* bias,
+                              void* H, void* Y, float* mean, float* rstd, msr_qfmt fmt,
+                              void* H_q, uint8_t* H_qs, void* B_q, uint8_t* B_qs,
+                              void* stream);
+
+/* Its backward: given dY and the gradient dH_in of H from its other uses
+ * (NULL: 0), with xh = (h - mean) rstd and g = dY (.) weight,
+ *   dH = dH_in + rstd (g - mean_d(g) [LAYER only] - xh mean_d(g xh))
+ *   dX = alpha dH,  dB = scale (.) dH
+ *   dscale = sum_rows dH b,  dweight = sum_rows dY xh,  dbias = sum_rows dY
+ * mean and rstd as the forward wrote them.  fmt names how H and B are held:
+ * MSR_Q_NONE, H [rows, d] in dtype and H_qs ignored; else H is H_q, H_qs of
+ * the forward (B likewise).  B is read for dscale only (then required).  dB,
+ * dscale, dweight, dbias may be NULL: not computed.
+ * Workspace (only where a sum is asked for): msr_resid_norm_bwd_workspace_bytes(). */
+msr_status msr_resid_norm_bwd(msr_dtype dtype, msr_norm norm, int32_t rows, int32_t d,
+                              float alpha, const void* dY, const void* dH_in, msr_qfmt fmt,
+                              const void* H, const uint8_t* H_qs, const void* B,
+                              const uint8_t* B_qs, const float* mean, const float* rstd,
+                              const float* scale, const float* weight, void* dX, void* dB,
+                              float* dscale, float* dweight, float* dbias, void* workspace,
+                              size_t ws_bytes, void* stream);
+size_t msr_resid_norm_bwd_workspace_bytes(int32_t rows, int32_t d);
+
+/* The norm after a retention core with its gate, per (row, head) over d_v:
+ *   n = (o - mu) r (.) weight_h + bias_h   (mu, r as above, of the head's o)
+ *   z = swish(g) (.) n,  swish(x) = x sigmoid(x)
+ * O, G, Z: [rows, heads, d_v] (dtype); weight, bias: [heads, d_v], NULL: 1,
+ * 0; mean, rstd: [rows, heads], may be NULL.  With fmt != MSR_Q_NONE, O and G
+ * are also kept in 8 bits (O_q, O_qs, G_q, G_qs).  d_v in {64, 128, 256,
+ * 512}, heads <= 128.  No workspace. */
+msr_status msr_gated_norm_fwd(msr_dtype dtype, msr_norm norm, int32_t rows, int32_t heads,
+                              int32_t d_v, float eps, const void* O, const void* G,
+                              const float* weight, const float* bias, void* Z, float* mean,
+                              float* rstd, msr_qfmt fmt, void* O_q, uint8_t* O_qs, void* G_q,
+                              uint8_t* G_qs, void* stream);
+
+/* Its backward, with xh = (o - mean) rstd, sg = sigmoid(g):
+ *   dn = dZ g sg,  u = dn (.) weight
+ *   dG = dZ n sg (1 + g (1 - sg))
+ *   dO = rstd (u - mean_dv(u) [LAYER only] - xh mean_dv(u xh))
+ *   dweight = sum_rows dn xh,  dbias = sum_rows dn
+ * O and G are held as fmt says (MSR_Q_NONE: in dtype, O_qs and G_qs
+ * ignored).  Z (NULL: not written) receives swish(g) (.) n again, the input
+ * of the projection behind it, for that projection's weight gradient.
+ * dweight, dbias may be NULL.  Workspace (only where a sum is asked for):
+ * msr_gated_norm_bwd_workspace_bytes(). */
+msr_status msr_gated_norm_bwd(msr_dtype dtype, msr_norm norm, int32_t rows, int32_t heads,
+                              int32_t d_v, const void* dZ, msr_qfmt fmt, const void* O,
+                              const uint8_t* O_qs, const void* G, const uint8_t* G_qs,
+                              const float* mean, const float* rstd, const float* weight,
+                              const float* bias, void* dO, void* dG, void* Z, float* dweight,
+                              float* dbias, void* workspace, size_t ws_bytes, void* stream);
+size_t msr_gated_norm_bwd_workspace_bytes(int32_t rows, int32_t heads, int32_t d_v);
+
+/* X [rows, cols] (dtype) to the 8-bit form; cols a multiple of 32.  q:
+ * [rows, cols] bytes, qs: [rows, cols / 32]. */
+msr_status msr_ckpt_pack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t cols,
+                         const void* X, void* q, uint8_t* qs, void* stream);
+
+/* The values read back into X [rows, cols] (dtype), normalised where any of
+ * the four is given: ((x - mean[row]) rstd[row]) weight[col] + bias[col]
+ * (NULL: 0, 1, 1, 0) -- Y of msr_resid_norm_fwd from its H_q. */
+msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t cols,
+                           const void* q, const uint8_t* qs, const float* mean,
+                           const float* rstd, const float* weight, const float* bias, void* X,
+                           void* stream);
+
+/* Weight gradient of a projection Y = X W whose input was kept in 8 bits:
+ *   dW = X^T dY  (accumulate != 0: dW += X^T dY),  float32 [d_in, d_out],
+ * X [rows, d_in] read back and normalised as in msr_ckpt_unpack and, where it
+ * is normalised, rounded to dtype; dY: [rows, d_out] (dtype).  d_in and
+ * d_out multiples of 64, at most 2^20; rows at most 2^22.
+ * Workspace: msr_ckpt_wgrad_workspace_bytes(). */
+msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in,
+                          int32_t d_out, const void* q, const uint8_t* qs, const float* mean,
+                          const float* rstd, const float* weight, const float* bias,
+                          const void* dY, int32_t accumulate, float* dW, void* workspace,
+                          size_t ws_bytes, void* stream);
+size_t msr_ckpt_wgrad_workspace_bytes(msr_dtype dtype, int32_t rows, int32_t d_in,
+                                      int32_t d_out, int32_t accumulate);
+
 /* Diagnostics for benchmarks: per-kernel timing with HIP events.
  * msr_trace_enable(1) clears earlier totals and from then on brackets every
  * kernel the library launches with an event pair recorded on that launch's

@@ -25,11 +25,17 @@ __all__ = [
     "msr_layer_decode_step", "msr_layer_decode_workspace_bytes",
     "msr_layer_decode_step_noalloc", "msr_layer_decode_noalloc_max_bytes",
     "msr_retnet_block_fwd", "msr_retnet_block_workspace_bytes",
+    "MSR_Q_NONE", "MSR_Q_E4M3", "MSR_Q_I8", "MSR_NORM_LAYER", "MSR_NORM_RMS",
+    "msr_resid_norm_fwd", "msr_resid_norm_bwd", "msr_resid_norm_bwd_workspace_bytes",
+    "msr_gated_norm_fwd", "msr_gated_norm_bwd", "msr_gated_norm_bwd_workspace_bytes",
+    "msr_ckpt_empty", "msr_ckpt_pack", "msr_ckpt_unpack", "msr_ckpt_wgrad", "msr_ckpt_wgrad_workspace_bytes",
     "msr_status_str", "msr_last_error", "msr_trace_enable", "msr_trace_count", "msr_trace_get",
     "trace_totals",
 ]
 
 MSR_F32, MSR_BF16 = 0, 1
+MSR_Q_NONE, MSR_Q_E4M3, MSR_Q_I8 = 0, 1, 2
+MSR_NORM_LAYER, MSR_NORM_RMS = 0, 1
 EXPORTS = (
     "msr_parallel_fwd", "msr_parallel_workspace_bytes", "msr_chunkwise_fwd",
     "msr_chunkwise_workspace_bytes", "msr_chunkwise_fwd_save", "msr_chunkwise_bwd",
@@ -37,7 +43,11 @@ EXPORTS = (
     "msr_rglru_fwd", "msr_rglru_workspace_bytes", "msr_recurrent_step", "msr_layer_fwd",
     "msr_layer_workspace_bytes", "msr_layer_decode_step", "msr_layer_decode_workspace_bytes",
     "msr_layer_decode_step_noalloc", "msr_layer_decode_noalloc_max_bytes",
-    "msr_retnet_block_fwd", "msr_retnet_block_workspace_bytes", "msr_status_str", "msr_last_error", "msr_trace_enable", "msr_trace_count", "msr_trace_get",
+    "msr_retnet_block_fwd", "msr_retnet_block_workspace_bytes",
+    "msr_resid_norm_fwd", "msr_resid_norm_bwd", "msr_resid_norm_bwd_workspace_bytes",
+    "msr_gated_norm_fwd", "msr_gated_norm_bwd", "msr_gated_norm_bwd_workspace_bytes",
+    "msr_ckpt_pack", "msr_ckpt_unpack", "msr_ckpt_wgrad", "msr_ckpt_wgrad_workspace_bytes",
+    "msr_status_str", "msr_last_error", "msr_trace_enable", "msr_trace_count", "msr_trace_get",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +119,16 @@ def lib():
         "msr_retnet_block_fwd": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _DP, _F, _F, _F,
                                         _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
         "msr_retnet_block_workspace_bytes": (_SZ, [_I32] * 9),
+        "msr_resid_norm_fwd": (_I32, [_I32, _I32, _I32, _I32, _F, _F] + [_P] * 9 + [_I32] + [_P] * 5),
+        "msr_resid_norm_bwd": (_I32, [_I32, _I32, _I32, _I32, _F, _P, _P, _I32] + [_P] * 13 + [_P, _SZ, _P]),
+        "msr_resid_norm_bwd_workspace_bytes": (_SZ, [_I32, _I32]),
+        "msr_gated_norm_fwd": (_I32, [_I32, _I32, _I32, _I32, _I32, _F] + [_P] * 7 + [_I32] + [_P] * 5),
+        "msr_gated_norm_bwd": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _I32] + [_P] * 13 + [_P, _SZ, _P]),
+        "msr_gated_norm_bwd_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+        "msr_ckpt_pack": (_I32, [_I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+        "msr_ckpt_unpack": (_I32, [_I32, _I32, _I32, _I32] + [_P] * 8),
+        "msr_ckpt_wgrad": (_I32, [_I32, _I32, _I32, _I32, _I32] + [_P] * 7 + [_I32, _P, _P, _SZ, _P]),
+        "msr_ckpt_wgrad_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
         "msr_trace_enable": (None, [_I32]),
         "msr_trace_count": (_I32, []),
         "msr_trace_get": (_I32, [_I32, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
@@ -541,3 +561,318 @@ def msr_layer_decode_step_noalloc(X, W_Q, W_K, W_V, W_G, W_O, S, gamma, heads, d
                                                _ptr(W_Q), _ptr(W_K), _ptr(W_V), _ptr(W_G), _ptr(W_O), _ptr(S),
                                                _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------- training between retention cores --
+class _On:
+    """The stream of a call and the tensors it allocates: with the tensors'
+    device current, on `stream` or that device's current stream.  Memory
+    allocated here for a stream other than the current one is recorded on it,
+    so that it is not handed out again before the call's work there is done."""
+
+    def __init__(self, t, stream):
+        torch = _torch()
+        self.device, self.other = t.device, None
+        if not t.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+        self.guard = None
+        if torch.cuda.current_device() != t.device.index:
+            self.guard = torch.cuda.device(t.device)
+            self.guard.__enter__()
+        cur = torch.cuda.current_stream()
+        self.handle = cur.cuda_stream
+        if stream is not None:
+            h = stream if isinstance(stream, int) else stream.cuda_stream
+            if h != self.handle:
+                self.handle = h
+                self.other = torch.cuda.ExternalStream(h, device=t.device) if isinstance(stream, int) else stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = _torch().empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+    def workspace(self, nbytes, workspace):
+        if nbytes == 0 or workspace is not None:
+            return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        return self.empty((nbytes,), _torch().uint8), nbytes
+
+
+def _q_format(name, q, qs, shape, device):
+    """The 8-bit format of a tensor by its type, its scale bytes checked."""
+    torch = _torch()
+    if qs is None:
+        raise ValueError(f"{name} in 8 bits needs its scale bytes")
+    if q.dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise ValueError(f"{name} must be torch.float8_e4m3fn or torch.int8, got {q.dtype}")
+    if shape[-1] % 32:
+        raise ValueError(f"the last dimension of {name} must be a multiple of 32")
+    _need(name, q, shape, q.dtype, device)
+    _need(name + " scale bytes", qs, (*shape[:-1], shape[-1] // 32), torch.uint8, device)
+    return MSR_Q_I8 if q.dtype == torch.int8 else MSR_Q_E4M3
+
+
+def _kept(shape, device, pairs):
+    """The common format of the given (name, q, qs) outputs (MSR_Q_NONE: none given)."""
+    fmt = MSR_Q_NONE
+    for name, q, qs in pairs:
+        if q is None and qs is None:
+            continue
+        if q is None:
+            raise ValueError(f"{name} scale bytes without {name}")
+        f = _q_format(name, q, qs, shape, device)
+        if fmt not in (MSR_Q_NONE, f):
+            raise ValueError("the tensors kept in 8 bits must share one format")
+        fmt = f
+    return fmt
+
+
+def _rows_of(shape):
+    n = 1
+    for s in shape:
+        n *= s
+    if n >= 2 ** 31:
+        raise ValueError("2^31 rows or more")
+    return n
+
+
+def msr_ckpt_empty(shape, fmt, device):
+    """Uninitialised (q, scale bytes) for a tensor of `shape` kept in 8 bits: q is float8_e4m3fn or int8, the
+    bytes (uint8) have one entry per 32 values of the last dimension."""
+    torch = _torch()
+    if fmt not in (MSR_Q_E4M3, MSR_Q_I8):
+        raise ValueError(f"unknown 8-bit format {fmt}")
+    if not shape or shape[-1] % 32:
+        raise ValueError("the last dimension must be a multiple of 32")
+    q = torch.empty(tuple(shape), dtype=torch.int8 if fmt == MSR_Q_I8 else torch.float8_e4m3fn, device=device)
+    return q, torch.empty((*shape[:-1], shape[-1] // 32), dtype=torch.uint8, device=device)
+
+
+def msr_resid_norm_fwd(X, B=None, *, scale=None, weight=None, bias=None, alpha=1.0, norm=MSR_NORM_LAYER, eps=1e-5,
+                       H=None, Y=None, mean=None, rstd=None, H_q=None, H_qs=None, B_q=None, B_qs=None, stream=None):
+    """h = alpha X + scale B (rounded to X's dtype), y = norm(h) weight + bias.  X, B: [..., d].  Returns (Y, H); H
+    is X itself where nothing is added or scaled and no H is given.  mean, rstd ([...] float32) and the 8-bit copies
+    (H_q, H_qs), (B_q, B_qs) (msr_ckpt_empty) are written if given."""
+    f32 = _torch().float32
+    d, lead = X.shape[-1], X.shape[:-1]
+    dt = _dtype_code(X)
+    _need("B", B, X.shape, X.dtype, X.device)
+    for name, t in (("scale", scale), ("weight", weight), ("bias", bias)):
+        _need(name, t, (d,), f32, X.device)
+    _need("H", H, X.shape, X.dtype, X.device)
+    _need("Y", Y, X.shape, X.dtype, X.device)
+    _need("mean", mean, lead, f32, X.device)
+    _need("rstd", rstd, lead, f32, X.device)
+    if B_q is not None and H_q is None:
+        raise ValueError("B_q without H_q")
+    fmt = _kept(X.shape, X.device, (("H_q", H_q, H_qs), ("B_q", B_q, B_qs)))
+    with _On(X, stream) as on:
+        Y = on.empty(X.shape, X.dtype) if Y is None else Y
+        same = H is None and B is None and alpha == 1.0
+        if H is None and not same:
+            H = on.empty(X.shape, X.dtype)
+        _check("msr_resid_norm_fwd",
+               lib().msr_resid_norm_fwd(dt, norm, _rows_of(lead), d, alpha, eps, _ptr(X), _ptr(B), _ptr(scale),
+                                        _ptr(weight), _ptr(bias), _ptr(H), _ptr(Y), _ptr(mean), _ptr(rstd), fmt,
+                                        _ptr(H_q), _ptr(H_qs), _ptr(B_q), _ptr(B_qs), on.handle))
+    return Y, X if same else H
+
+
+def msr_resid_norm_bwd_workspace_bytes(rows, d) -> int:
+    return lib().msr_resid_norm_bwd_workspace_bytes(rows, d)
+
+
+def _held(name, t, ts, like):
+    """Checks a tensor held in like's dtype (ts None) or in 8 bits; returns its format."""
+    if ts is None:
+        _need(name, t, like.shape, like.dtype, like.device)
+        return MSR_Q_NONE
+    return _q_format(name, t, ts, like.shape, like.device)
+
+
+def msr_resid_norm_bwd(dY, H, mean, rstd, *, H_qs=None, dH=None, B=None, B_qs=None, scale=None, weight=None,
+                       alpha=1.0, norm=MSR_NORM_LAYER, dX=None, dB=None, dscale=None, dweight=None, dbias=None,
+                       workspace=None, stream=None):
+    """Backward of msr_resid_norm_fwd.  H: the forward's H, or its H_q with H_qs; mean (None for MSR_NORM_RMS),
+    rstd: the forward's; dH: the gradient of H from its other uses.  Returns dX; dB, dscale, dweight, dbias are
+    written if given (dscale needs B, or B_q with B_qs)."""
+    f32 = _torch().float32
+    d, lead = dY.shape[-1], dY.shape[:-1]
+    dt = _dtype_code(dY)
+    if H is None or rstd is None or (mean is None and norm == MSR_NORM_LAYER):
+        raise ValueError("H, rstd and (MSR_NORM_LAYER) mean are required")
+    fmt = _held("H", H, H_qs, dY)
+    if B is not None and _held("B", B, B_qs, dY) != fmt:
+        raise ValueError("B must be held as H is")
+    _need("dH", dH, dY.shape, dY.dtype, dY.device)
+    _need("mean", mean, lead, f32, dY.device)
+    _need("rstd", rstd, lead, f32, dY.device)
+    for name, t in (("scale", scale), ("weight", weight), ("dscale", dscale), ("dweight", dweight),
+                    ("dbias", dbias)):
+        _need(name, t, (d,), f32, dY.device)
+    _need("dX", dX, dY.shape, dY.dtype, dY.device)
+    _need("dB", dB, dY.shape, dY.dtype, dY.device)
+    _need_ws(workspace, dY.device)
+    rows = _rows_of(lead)
+    with _On(dY, stream) as on:
+        dX = on.empty(dY.shape, dY.dtype) if dX is None else dX
+        sums = dscale is not None or dweight is not None or dbias is not None
+        ws, wsb = on.workspace(lib().msr_resid_norm_bwd_workspace_bytes(rows, d) if sums else 0, workspace)
+        _check("msr_resid_norm_bwd",
+               lib().msr_resid_norm_bwd(dt, norm, rows, d, alpha, _ptr(dY), _ptr(dH), fmt, _ptr(H), _ptr(H_qs),
+                                        _ptr(B), _ptr(B_qs), _ptr(mean), _ptr(rstd), _ptr(scale), _ptr(weight),
+                                        _ptr(dX), _ptr(dB), _ptr(dscale), _ptr(dweight), _ptr(dbias), _ptr(ws), wsb,
+                                        on.handle))
+    return dX
+
+
+def msr_gated_norm_fwd(O, G, *, weight=None, bias=None, norm=MSR_NORM_LAYER, eps=1e-5, Z=None, mean=None, rstd=None,
+                       O_q=None, O_qs=None, G_q=None, G_qs=None, stream=None):
+    """Z = swish(G) (norm_h(O) weight + bias), per head.  O, G: [..., heads, d_v]; weight, bias: [heads, d_v]
+    float32.  Returns Z; mean, rstd ([..., heads] float32) and the 8-bit copies (O_q, O_qs) and (G_q, G_qs)
+    (both or neither) are written if given."""
+    f32 = _torch().float32
+    heads, dv = O.shape[-2:]
+    lead = O.shape[:-1]
+    dt = _dtype_code(O)
+    _need("G", G, O.shape, O.dtype, O.device)
+    _need("weight", weight, (heads, dv), f32, O.device)
+    _need("bias", bias, (heads, dv), f32, O.device)
+    _need("Z", Z, O.shape, O.dtype, O.device)
+    _need("mean", mean, lead, f32, O.device)
+    _need("rstd", rstd, lead, f32, O.device)
+    if (O_q is None) != (G_q is None):
+        raise ValueError("O_q and G_q go together")
+    fmt = _kept(O.shape, O.device, (("O_q", O_q, O_qs), ("G_q", G_q, G_qs)))
+    with _On(O, stream) as on:
+        Z = on.empty(O.shape, O.dtype) if Z is None else Z
+        _check("msr_gated_norm_fwd",
+               lib().msr_gated_norm_fwd(dt, norm, _rows_of(O.shape[:-2]), heads, dv, eps, _ptr(O), _ptr(G),
+                                        _ptr(weight), _ptr(bias), _ptr(Z), _ptr(mean), _ptr(rstd), fmt, _ptr(O_q),
+                                        _ptr(O_qs), _ptr(G_q), _ptr(G_qs), on.handle))
+    return Z
+
+
+def msr_gated_norm_bwd_workspace_bytes(rows, heads, d_v) -> int:
+    return lib().msr_gated_norm_bwd_workspace_bytes(rows, heads, d_v)
+
+
+def msr_gated_norm_bwd(dZ, O, G, mean, rstd, *, O_qs=None, G_qs=None, weight=None, bias=None, norm=MSR_NORM_LAYER,
+                       dO=None, dG=None, Z=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """Backward of msr_gated_norm_fwd.  O, G: the forward's, or its O_q and G_q with O_qs and G_qs; mean (None for
+    MSR_NORM_RMS), rstd: the forward's.  Returns (dO, dG); Z (the forward's output again), dweight and dbias are
+    written if given."""
+    f32 = _torch().float32
+    heads, dv = dZ.shape[-2:]
+    lead = dZ.shape[:-1]
+    dt = _dtype_code(dZ)
+    if O is None or G is None or rstd is None or (mean is None and norm == MSR_NORM_LAYER):
+        raise ValueError("O, G, rstd and (MSR_NORM_LAYER) mean are required")
+    fmt = _held("O", O, O_qs, dZ)
+    if _held("G", G, G_qs, dZ) != fmt:
+        raise ValueError("G must be held as O is")
+    _need("mean", mean, lead, f32, dZ.device)
+    _need("rstd", rstd, lead, f32, dZ.device)
+    for name, t in (("weight", weight), ("bias", bias), ("dweight", dweight), ("dbias", dbias)):
+        _need(name, t, (heads, dv), f32, dZ.device)
+    for name, t in (("dO", dO), ("dG", dG), ("Z", Z)):
+        _need(name, t, dZ.shape, dZ.dtype, dZ.device)
+    _need_ws(workspace, dZ.device)
+    rows = _rows_of(dZ.shape[:-2])
+    with _On(dZ, stream) as on:
+        dO = on.empty(dZ.shape, dZ.dtype) if dO is None else dO
+        dG = on.empty(dZ.shape, dZ.dtype) if dG is None else dG
+        sums = dweight is not None or dbias is not None
+        ws, wsb = on.workspace(lib().msr_gated_norm_bwd_workspace_bytes(rows, heads, dv) if sums else 0, workspace)
+        _check("msr_gated_norm_bwd",
+               lib().msr_gated_norm_bwd(dt, norm, rows, heads, dv, _ptr(dZ), fmt, _ptr(O), _ptr(O_qs), _ptr(G),
+                                        _ptr(G_qs), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(dO),
+                                        _ptr(dG), _ptr(Z), _ptr(dweight), _ptr(dbias), _ptr(ws), wsb, on.handle))
+    return dO, dG
+
+
+def msr_ckpt_pack(X, fmt=MSR_Q_E4M3, *, q=None, qs=None, stream=None):
+    """X [..., cols] in 8 bits.  Returns (q, qs), allocated as msr_ckpt_empty does where not given."""
+    torch = _torch()
+    dt = _dtype_code(X)
+    if fmt not in (MSR_Q_E4M3, MSR_Q_I8):
+        raise ValueError(f"unknown 8-bit format {fmt}")
+    if X.dim() == 0 or X.shape[-1] % 32:
+        raise ValueError("the last dimension must be a multiple of 32")
+    cols, lead = X.shape[-1], X.shape[:-1]
+    qt = torch.int8 if fmt == MSR_Q_I8 else torch.float8_e4m3fn
+    _need("q", q, X.shape, qt, X.device)
+    _need("qs", qs, (*lead, cols // 32), torch.uint8, X.device)
+    with _On(X, stream) as on:
+        q = on.empty(X.shape, qt) if q is None else q
+        qs = on.empty((*lead, cols // 32), torch.uint8) if qs is None else qs
+        _check("msr_ckpt_pack", lib().msr_ckpt_pack(dt, fmt, _rows_of(lead), cols, _ptr(X), _ptr(q), _ptr(qs),
+                                                    on.handle))
+    return q, qs
+
+
+def msr_ckpt_unpack(q, qs, dtype=None, *, mean=None, rstd=None, weight=None, bias=None, out=None, stream=None):
+    """The values of (q, qs) in `dtype` (torch.bfloat16 or torch.float32; default: out's, else bfloat16), normalised
+    where any of mean, rstd ([...]), weight, bias ([cols], float32) is given.  Returns them."""
+    torch = _torch()
+    f32 = torch.float32
+    fmt = _q_format("q", q, qs, q.shape, q.device)
+    cols, lead = q.shape[-1], q.shape[:-1]
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    if dtype not in (torch.bfloat16, f32):
+        raise TypeError(f"unsupported tensor dtype {dtype}; use float32 or bfloat16")
+    _need("out", out, q.shape, dtype, q.device)
+    _need("mean", mean, lead, f32, q.device)
+    _need("rstd", rstd, lead, f32, q.device)
+    _need("weight", weight, (cols,), f32, q.device)
+    _need("bias", bias, (cols,), f32, q.device)
+    with _On(q, stream) as on:
+        out = on.empty(q.shape, dtype) if out is None else out
+        _check("msr_ckpt_unpack",
+               lib().msr_ckpt_unpack(MSR_F32 if dtype == f32 else MSR_BF16, fmt, _rows_of(lead), cols, _ptr(q),
+                                     _ptr(qs), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(out),
+                                     on.handle))
+    return out
+
+
+def msr_ckpt_wgrad_workspace_bytes(dtype: int, rows, d_in, d_out, accumulate=False) -> int:
+    return lib().msr_ckpt_wgrad_workspace_bytes(dtype, rows, d_in, d_out, 1 if accumulate else 0)
+
+
+def msr_ckpt_wgrad(q, qs, dY, *, mean=None, rstd=None, weight=None, bias=None, dW=None, accumulate=False,
+                   workspace=None, stream=None):
+    """dW = X^T dY (accumulate: dW += X^T dY), X [..., d_in] kept in 8 bits as (q, qs) and normalised as in
+    msr_ckpt_unpack; dY: [..., d_out].  Returns dW [d_in, d_out] float32."""
+    f32 = _torch().float32
+    fmt = _q_format("q", q, qs, q.shape, dY.device)
+    d_in, lead = q.shape[-1], q.shape[:-1]
+    d_out = dY.shape[-1]
+    dt = _dtype_code(dY)
+    _need("dY", dY, (*lead, d_out), dY.dtype, dY.device)
+    _need("mean", mean, lead, f32, dY.device)
+    _need("rstd", rstd, lead, f32, dY.device)
+    _need("weight", weight, (d_in,), f32, dY.device)
+    _need("bias", bias, (d_in,), f32, dY.device)
+    _need("dW", dW, (d_in, d_out), f32, dY.device)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    _need_ws(workspace, dY.device)
+    rows = _rows_of(lead)
+    with _On(dY, stream) as on:
+        dW = on.empty((d_in, d_out), f32) if dW is None else dW
+        ws, wsb = on.workspace(lib().msr_ckpt_wgrad_workspace_bytes(dt, rows, d_in, d_out, 1 if accumulate else 0),
+                               workspace)
+        _check("msr_ckpt_wgrad",
+               lib().msr_ckpt_wgrad(dt, fmt, rows, d_in, d_out, _ptr(q), _ptr(qs), _ptr(mean), _ptr(rstd),
+                                    _ptr(weight), _ptr(bias), _ptr(dY), 1 if accumulate else 0, _ptr(dW), _ptr(ws),
+                                    wsb, on.handle))
+    return dW

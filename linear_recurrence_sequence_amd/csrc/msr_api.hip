@@ -10,14 +10,16 @@
 
 #include "../../include/msr.h"
 #include "msr_launch.h"
+#include "msr_status.h"
 
 using namespace msr;
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
-msr_status fail(msr_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace msr {
+
 msr_status fail(msr_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -37,6 +39,10 @@ msr_status from_hip(hipError_t e, const char* where) {
   if (e == hipSuccess) return ok();
   return fail(MSR_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
+
+}  // namespace msr
+
+namespace {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }

@@ -187,4 +187,107 @@ int gemm_splits(Elt elt, int M, int N, int K);
 hipError_t launch_layer_norm(Elt elt, const void* X, int64_t ldx, void* Y, int64_t ldy, int rows, int d, float eps,
                              hipStream_t stream);
 
+// ---- norms between retention cores, with gate and residual (k_norm.hip) ----
+// fmt: kQNone (activations in elt) or the 8-bit format of the *_q / *_qs
+// pairs (msr_q8.h).  Nullable pointers are named.
+struct ResidNormArgs {
+  Elt elt;
+  int fmt;
+  bool layer;                                        // mean subtracted
+  int64_t rows;
+  int d;                                             // multiple of 64, at most 8192
+  float alpha, eps;
+  const void* X; const void* B;                      // B null: h = alpha x
+  const float* scale; const float* weight; const float* bias;   // [d], null: 1, 1, 0
+  void* H; void* Y;                                  // H null: not written
+  float* mean; float* rstd;                          // [rows], null: not written
+  uint8_t* H_q; uint8_t* H_qs;                       // with fmt
+  uint8_t* B_q; uint8_t* B_qs;                       // with fmt, null: not written
+};
+hipError_t launch_resid_norm_fwd(const ResidNormArgs& a, hipStream_t st);
+struct ResidNormBwdArgs {
+  Elt elt;
+  int fmt;                                           // of H and B
+  bool layer;
+  int64_t rows;
+  int d;
+  float alpha;
+  const void* dY; const void* dH_in;                 // dH_in null: 0
+  const void* H; const uint8_t* H_qs;
+  const void* B; const uint8_t* B_qs;                // only with dscale
+  const float* mean; const float* rstd;
+  const float* scale; const float* weight;
+  void* dX; void* dB;                                // dB null: not written
+  float* part;                                       // resid_norm_bwd_parts() rows of d per requested sum
+  bool sum_w, sum_c;                                 // set by the launcher
+};
+int resid_norm_bwd_parts(int64_t rows, int d);
+// dscale, dweight, dbias null: not computed
+hipError_t launch_resid_norm_bwd(const ResidNormBwdArgs& a, float* dscale, float* dweight, float* dbias,
+                                 hipStream_t st);
+struct GatedNormArgs {
+  Elt elt;
+  int fmt;
+  bool layer;
+  int64_t rows;
+  int heads, d_v;                                    // d_v 64, 128, 256 or 512
+  float eps;
+  const void* O; const void* G;
+  const float* weight; const float* bias;            // [heads, d_v], nullable
+  void* Z;
+  float* mean; float* rstd;                          // [rows, heads], nullable
+  uint8_t* O_q; uint8_t* O_qs; uint8_t* G_q; uint8_t* G_qs;   // with fmt
+  int R;                                             // set by the launcher
+};
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t st);
+struct GatedNormBwdArgs {
+  Elt elt;
+  int fmt;                                           // of O and G
+  bool layer;
+  int64_t rows;
+  int heads, d_v;
+  const void* dZ;
+  const void* O; const uint8_t* O_qs;
+  const void* G; const uint8_t* G_qs;
+  const float* mean; const float* rstd;
+  const float* weight; const float* bias;
+  void* dO; void* dG; void* Z;                       // Z null: not written
+  float* part;                                       // gated_norm_bwd_parts() rows of heads * d_v per requested sum
+  bool sum_w, sum_c;                                 // set by the launcher
+  int R;
+};
+int gated_norm_bwd_parts(int64_t rows, int heads, int d_v);
+hipError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, float* dweight, float* dbias, hipStream_t st);
+// out.v[i][j] = sum over p < P of part[i][p][j], i < vecs <= 3, j < n.
+struct ColSumOut {
+  float* v[3];
+};
+hipError_t launch_col_sums(const float* part, int P, int n, const ColSumOut& out, int vecs, hipStream_t st);
+
+// ---- activations held in 8 bits (k_ckpt.hip) ----
+hipError_t launch_ckpt_pack(Elt elt, int fmt, int64_t rows, int cols, const void* X, uint8_t* q, uint8_t* qs,
+                            hipStream_t st);
+// The values read back, optionally normalised: ((x - mean[row]) rstd[row])
+// weight[col] + bias[col] (each nullable: 0, 1, 1, 0).
+struct CkptArgs {
+  int64_t rows;
+  int cols;
+  const uint8_t* q; const uint8_t* qs;
+  const float* mean; const float* rstd; const float* weight; const float* bias;
+};
+hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipStream_t st);
+// Their transpose: XT[col][row], row stride ld (a multiple of 64, >= rows),
+// zeros in columns rows .. ld - 1; cols a multiple of 64.
+hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, hipStream_t st);
+// dst[r][c] = src[r][c] for r < rows, 0 for rows <= r < rows_out; contiguous
+// rows of cols (a multiple of 8).
+hipError_t launch_pad_rows(Elt elt, const void* src, void* dst, int64_t rows, int64_t rows_out, int cols,
+                           hipStream_t st);
+// out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
+hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
+// float32 products of K slices: part[z M N + m N + n] = sum over the K rows
+// [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K a multiple of 64, N of 8.
+hipError_t launch_gemm_parts(Elt elt, const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M,
+                             int N, int K, int splits, hipStream_t st);
+
 }  // namespace msr

@@ -5,9 +5,10 @@ the ``cpu_baseline`` leg of ``bench.py`` may import this package.  It shares
 no code with the HIP library and imports nothing from it.
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
+(those of ``oracle.training`` by ``tests/test_training_pins.py``)
 against closed forms, exact rational brute force, the pages' stated
-equivalences between the three forms, and GroupNorm scale invariance.  No
-function is "parity unpinned".
+equivalences between the three forms, differences, and GroupNorm scale
+invariance.  No function is "parity unpinned".
 """
 from .retention import (  # noqa: F401
     rotary,
