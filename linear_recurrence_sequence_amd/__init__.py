@@ -569,18 +569,18 @@ class _On:
     device current, on `stream` or that device's current stream.  Memory
     allocated here for a stream other than the current one is recorded on it,
     so that it is not handed out again before the call's work there is done."""
+    __slots__ = ("torch", "device", "guard", "handle", "other")
 
     def __init__(self, t, stream):
-        torch = _torch()
-        self.device, self.other = t.device, None
+        torch = self.torch = _torch()
         if not t.is_cuda:
             raise ValueError("tensors must be on the GPU")
-        self.guard = None
+        self.device = t.device
+        self.guard = self.other = None
         if torch.cuda.current_device() != t.device.index:
             self.guard = torch.cuda.device(t.device)
             self.guard.__enter__()
-        cur = torch.cuda.current_stream()
-        self.handle = cur.cuda_stream
+        self.handle = torch.cuda.current_stream().cuda_stream
         if stream is not None:
             h = stream if isinstance(stream, int) else stream.cuda_stream
             if h != self.handle:
@@ -595,44 +595,70 @@ class _On:
             self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        t = _torch().empty(shape, dtype=dtype, device=self.device)
+        t = self.torch.empty(shape, dtype=dtype, device=self.device)
         if self.other is not None:
             t.record_stream(self.other)
         return t
 
     def workspace(self, nbytes, workspace):
-        if nbytes == 0 or workspace is not None:
-            return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-        return self.empty((nbytes,), _torch().uint8), nbytes
+        """(pointer, bytes, tensor to keep) of the caller's workspace, or of one of nbytes allocated here."""
+        if workspace is None:
+            if nbytes == 0:
+                return None, 0, None
+            workspace = self.empty((nbytes,), self.torch.uint8)
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _q_format(name, q, qs, shape, device):
-    """The 8-bit format of a tensor by its type, its scale bytes checked."""
+def _args(device, *specs):
+    """Pointers of (name, tensor, shape, dtype) arguments after _need's checks and contiguity; None stays None."""
+    out = []
+    for name, t, shape, dtype in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or t.device != device:
+            _need(name, t, shape, dtype, device)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _q_format(name, q, qs, shape):
+    """The 8-bit format of a tensor by its type, and the shape of its scale bytes."""
     torch = _torch()
+    if q is None:
+        raise ValueError(f"{name} scale bytes without {name}")
     if qs is None:
         raise ValueError(f"{name} in 8 bits needs its scale bytes")
     if q.dtype not in (torch.float8_e4m3fn, torch.int8):
         raise ValueError(f"{name} must be torch.float8_e4m3fn or torch.int8, got {q.dtype}")
-    if shape[-1] % 32:
+    if not shape or shape[-1] % 32:
         raise ValueError(f"the last dimension of {name} must be a multiple of 32")
-    _need(name, q, shape, q.dtype, device)
-    _need(name + " scale bytes", qs, (*shape[:-1], shape[-1] // 32), torch.uint8, device)
     return MSR_Q_I8 if q.dtype == torch.int8 else MSR_Q_E4M3
 
 
-def _kept(shape, device, pairs):
-    """The common format of the given (name, q, qs) outputs (MSR_Q_NONE: none given)."""
-    fmt = MSR_Q_NONE
+def _kept(device, shape, *pairs):
+    """The common format (MSR_Q_NONE: none given) and the pointers, pair by pair, of (name, q, scale bytes) outputs."""
+    fmt, out = MSR_Q_NONE, []
     for name, q, qs in pairs:
         if q is None and qs is None:
+            out += [None, None]
             continue
-        if q is None:
-            raise ValueError(f"{name} scale bytes without {name}")
-        f = _q_format(name, q, qs, shape, device)
+        f = _q_format(name, q, qs, shape)
         if fmt not in (MSR_Q_NONE, f):
             raise ValueError("the tensors kept in 8 bits must share one format")
         fmt = f
-    return fmt
+        out += _args(device, (name, q, shape, q.dtype),
+                     (name + " scale bytes", qs, (*shape[:-1], shape[-1] // 32), _torch().uint8))
+    return fmt, out
+
+
+def _held(device, name, t, ts, like):
+    """Format and pointers of a tensor held in like's dtype (ts None) or in 8 bits."""
+    if ts is None:
+        return MSR_Q_NONE, _args(device, (name, t, like.shape, like.dtype)) + [None]
+    return _kept(device, like.shape, (name, t, ts))
 
 
 def _rows_of(shape):
@@ -661,41 +687,32 @@ def msr_resid_norm_fwd(X, B=None, *, scale=None, weight=None, bias=None, alpha=1
     """h = alpha X + scale B (rounded to X's dtype), y = norm(h) weight + bias.  X, B: [..., d].  Returns (Y, H); H
     is X itself where nothing is added or scaled and no H is given.  mean, rstd ([...] float32) and the 8-bit copies
     (H_q, H_qs), (B_q, B_qs) (msr_ckpt_empty) are written if given."""
-    f32 = _torch().float32
-    d, lead = X.shape[-1], X.shape[:-1]
+    f32, dev, shape, ty = _torch().float32, X.device, X.shape, X.dtype
+    d, lead = shape[-1], shape[:-1]
     dt = _dtype_code(X)
-    _need("B", B, X.shape, X.dtype, X.device)
-    for name, t in (("scale", scale), ("weight", weight), ("bias", bias)):
-        _need(name, t, (d,), f32, X.device)
-    _need("H", H, X.shape, X.dtype, X.device)
-    _need("Y", Y, X.shape, X.dtype, X.device)
-    _need("mean", mean, lead, f32, X.device)
-    _need("rstd", rstd, lead, f32, X.device)
     if B_q is not None and H_q is None:
         raise ValueError("B_q without H_q")
-    fmt = _kept(X.shape, X.device, (("H_q", H_q, H_qs), ("B_q", B_q, B_qs)))
+    same = H is None and B is None and alpha == 1.0
+    pX, pB, ps, pw, pc, pH, pY, pm, pr = _args(
+        dev, ("X", X, shape, ty), ("B", B, shape, ty), ("scale", scale, (d,), f32), ("weight", weight, (d,), f32),
+        ("bias", bias, (d,), f32), ("H", H, shape, ty), ("Y", Y, shape, ty), ("mean", mean, lead, f32),
+        ("rstd", rstd, lead, f32))
+    fmt, kept = _kept(dev, shape, ("H_q", H_q, H_qs), ("B_q", B_q, B_qs))
     with _On(X, stream) as on:
-        Y = on.empty(X.shape, X.dtype) if Y is None else Y
-        same = H is None and B is None and alpha == 1.0
+        if Y is None:
+            Y = on.empty(shape, ty)
+            pY = Y.data_ptr()
         if H is None and not same:
-            H = on.empty(X.shape, X.dtype)
+            H = on.empty(shape, ty)
+            pH = H.data_ptr()
         _check("msr_resid_norm_fwd",
-               lib().msr_resid_norm_fwd(dt, norm, _rows_of(lead), d, alpha, eps, _ptr(X), _ptr(B), _ptr(scale),
-                                        _ptr(weight), _ptr(bias), _ptr(H), _ptr(Y), _ptr(mean), _ptr(rstd), fmt,
-                                        _ptr(H_q), _ptr(H_qs), _ptr(B_q), _ptr(B_qs), on.handle))
+               lib().msr_resid_norm_fwd(dt, norm, _rows_of(lead), d, alpha, eps, pX, pB, ps, pw, pc, pH, pY, pm, pr,
+                                        fmt, *kept, on.handle))
     return Y, X if same else H
 
 
 def msr_resid_norm_bwd_workspace_bytes(rows, d) -> int:
     return lib().msr_resid_norm_bwd_workspace_bytes(rows, d)
-
-
-def _held(name, t, ts, like):
-    """Checks a tensor held in like's dtype (ts None) or in 8 bits; returns its format."""
-    if ts is None:
-        _need(name, t, like.shape, like.dtype, like.device)
-        return MSR_Q_NONE
-    return _q_format(name, t, ts, like.shape, like.device)
 
 
 def msr_resid_norm_bwd(dY, H, mean, rstd, *, H_qs=None, dH=None, B=None, B_qs=None, scale=None, weight=None,
@@ -704,33 +721,32 @@ def msr_resid_norm_bwd(dY, H, mean, rstd, *, H_qs=None, dH=None, B=None, B_qs=No
     """Backward of msr_resid_norm_fwd.  H: the forward's H, or its H_q with H_qs; mean (None for MSR_NORM_RMS),
     rstd: the forward's; dH: the gradient of H from its other uses.  Returns dX; dB, dscale, dweight, dbias are
     written if given (dscale needs B, or B_q with B_qs)."""
-    f32 = _torch().float32
-    d, lead = dY.shape[-1], dY.shape[:-1]
+    f32, dev, shape, ty = _torch().float32, dY.device, dY.shape, dY.dtype
+    d, lead = shape[-1], shape[:-1]
     dt = _dtype_code(dY)
     if H is None or rstd is None or (mean is None and norm == MSR_NORM_LAYER):
         raise ValueError("H, rstd and (MSR_NORM_LAYER) mean are required")
-    fmt = _held("H", H, H_qs, dY)
-    if B is not None and _held("B", B, B_qs, dY) != fmt:
-        raise ValueError("B must be held as H is")
-    _need("dH", dH, dY.shape, dY.dtype, dY.device)
-    _need("mean", mean, lead, f32, dY.device)
-    _need("rstd", rstd, lead, f32, dY.device)
-    for name, t in (("scale", scale), ("weight", weight), ("dscale", dscale), ("dweight", dweight),
-                    ("dbias", dbias)):
-        _need(name, t, (d,), f32, dY.device)
-    _need("dX", dX, dY.shape, dY.dtype, dY.device)
-    _need("dB", dB, dY.shape, dY.dtype, dY.device)
-    _need_ws(workspace, dY.device)
+    fmt, (pH, pHs) = _held(dev, "H", H, H_qs, dY)
+    pB = pBs = None
+    if B is not None or B_qs is not None:
+        fb, (pB, pBs) = _held(dev, "B", B, B_qs, dY)
+        if fb != fmt:
+            raise ValueError("B must be held as H is")
+    pY, pd, pm, pr, ps, pw, pX, pdB, pds, pdw, pdc = _args(
+        dev, ("dY", dY, shape, ty), ("dH", dH, shape, ty), ("mean", mean, lead, f32), ("rstd", rstd, lead, f32),
+        ("scale", scale, (d,), f32), ("weight", weight, (d,), f32), ("dX", dX, shape, ty), ("dB", dB, shape, ty),
+        ("dscale", dscale, (d,), f32), ("dweight", dweight, (d,), f32), ("dbias", dbias, (d,), f32))
+    _need_ws(workspace, dev)
     rows = _rows_of(lead)
     with _On(dY, stream) as on:
-        dX = on.empty(dY.shape, dY.dtype) if dX is None else dX
-        sums = dscale is not None or dweight is not None or dbias is not None
-        ws, wsb = on.workspace(lib().msr_resid_norm_bwd_workspace_bytes(rows, d) if sums else 0, workspace)
+        if dX is None:
+            dX = on.empty(shape, ty)
+            pX = dX.data_ptr()
+        need = 0 if pds is pdw is pdc is None else lib().msr_resid_norm_bwd_workspace_bytes(rows, d)
+        ws, wsb, _keep = on.workspace(need, workspace)
         _check("msr_resid_norm_bwd",
-               lib().msr_resid_norm_bwd(dt, norm, rows, d, alpha, _ptr(dY), _ptr(dH), fmt, _ptr(H), _ptr(H_qs),
-                                        _ptr(B), _ptr(B_qs), _ptr(mean), _ptr(rstd), _ptr(scale), _ptr(weight),
-                                        _ptr(dX), _ptr(dB), _ptr(dscale), _ptr(dweight), _ptr(dbias), _ptr(ws), wsb,
-                                        on.handle))
+               lib().msr_resid_norm_bwd(dt, norm, rows, d, alpha, pY, pd, fmt, pH, pHs, pB, pBs, pm, pr, ps, pw, pX,
+                                        pdB, pds, pdw, pdc, ws, wsb, on.handle))
     return dX
 
 
@@ -739,25 +755,23 @@ def msr_gated_norm_fwd(O, G, *, weight=None, bias=None, norm=MSR_NORM_LAYER, eps
     """Z = swish(G) (norm_h(O) weight + bias), per head.  O, G: [..., heads, d_v]; weight, bias: [heads, d_v]
     float32.  Returns Z; mean, rstd ([..., heads] float32) and the 8-bit copies (O_q, O_qs) and (G_q, G_qs)
     (both or neither) are written if given."""
-    f32 = _torch().float32
-    heads, dv = O.shape[-2:]
-    lead = O.shape[:-1]
+    f32, dev, shape, ty = _torch().float32, O.device, O.shape, O.dtype
+    heads, dv = shape[-2:]
+    lead = shape[:-1]
     dt = _dtype_code(O)
-    _need("G", G, O.shape, O.dtype, O.device)
-    _need("weight", weight, (heads, dv), f32, O.device)
-    _need("bias", bias, (heads, dv), f32, O.device)
-    _need("Z", Z, O.shape, O.dtype, O.device)
-    _need("mean", mean, lead, f32, O.device)
-    _need("rstd", rstd, lead, f32, O.device)
     if (O_q is None) != (G_q is None):
         raise ValueError("O_q and G_q go together")
-    fmt = _kept(O.shape, O.device, (("O_q", O_q, O_qs), ("G_q", G_q, G_qs)))
+    pO, pG, pw, pc, pZ, pm, pr = _args(
+        dev, ("O", O, shape, ty), ("G", G, shape, ty), ("weight", weight, (heads, dv), f32),
+        ("bias", bias, (heads, dv), f32), ("Z", Z, shape, ty), ("mean", mean, lead, f32), ("rstd", rstd, lead, f32))
+    fmt, kept = _kept(dev, shape, ("O_q", O_q, O_qs), ("G_q", G_q, G_qs))
     with _On(O, stream) as on:
-        Z = on.empty(O.shape, O.dtype) if Z is None else Z
+        if Z is None:
+            Z = on.empty(shape, ty)
+            pZ = Z.data_ptr()
         _check("msr_gated_norm_fwd",
-               lib().msr_gated_norm_fwd(dt, norm, _rows_of(O.shape[:-2]), heads, dv, eps, _ptr(O), _ptr(G),
-                                        _ptr(weight), _ptr(bias), _ptr(Z), _ptr(mean), _ptr(rstd), fmt, _ptr(O_q),
-                                        _ptr(O_qs), _ptr(G_q), _ptr(G_qs), on.handle))
+               lib().msr_gated_norm_fwd(dt, norm, _rows_of(shape[:-2]), heads, dv, eps, pO, pG, pw, pc, pZ, pm, pr,
+                                        fmt, *kept, on.handle))
     return Z
 
 
@@ -770,77 +784,80 @@ def msr_gated_norm_bwd(dZ, O, G, mean, rstd, *, O_qs=None, G_qs=None, weight=Non
     """Backward of msr_gated_norm_fwd.  O, G: the forward's, or its O_q and G_q with O_qs and G_qs; mean (None for
     MSR_NORM_RMS), rstd: the forward's.  Returns (dO, dG); Z (the forward's output again), dweight and dbias are
     written if given."""
-    f32 = _torch().float32
-    heads, dv = dZ.shape[-2:]
-    lead = dZ.shape[:-1]
+    f32, dev, shape, ty = _torch().float32, dZ.device, dZ.shape, dZ.dtype
+    heads, dv = shape[-2:]
+    lead = shape[:-1]
     dt = _dtype_code(dZ)
     if O is None or G is None or rstd is None or (mean is None and norm == MSR_NORM_LAYER):
         raise ValueError("O, G, rstd and (MSR_NORM_LAYER) mean are required")
-    fmt = _held("O", O, O_qs, dZ)
-    if _held("G", G, G_qs, dZ) != fmt:
+    fmt, (pO, pOs) = _held(dev, "O", O, O_qs, dZ)
+    fg, (pG, pGs) = _held(dev, "G", G, G_qs, dZ)
+    if fg != fmt:
         raise ValueError("G must be held as O is")
-    _need("mean", mean, lead, f32, dZ.device)
-    _need("rstd", rstd, lead, f32, dZ.device)
-    for name, t in (("weight", weight), ("bias", bias), ("dweight", dweight), ("dbias", dbias)):
-        _need(name, t, (heads, dv), f32, dZ.device)
-    for name, t in (("dO", dO), ("dG", dG), ("Z", Z)):
-        _need(name, t, dZ.shape, dZ.dtype, dZ.device)
-    _need_ws(workspace, dZ.device)
-    rows = _rows_of(dZ.shape[:-2])
+    vec = (heads, dv)
+    pz, pm, pr, pw, pc, pdO, pdG, pZ, pdw, pdc = _args(
+        dev, ("dZ", dZ, shape, ty), ("mean", mean, lead, f32), ("rstd", rstd, lead, f32),
+        ("weight", weight, vec, f32), ("bias", bias, vec, f32), ("dO", dO, shape, ty), ("dG", dG, shape, ty),
+        ("Z", Z, shape, ty), ("dweight", dweight, vec, f32), ("dbias", dbias, vec, f32))
+    _need_ws(workspace, dev)
+    rows = _rows_of(shape[:-2])
     with _On(dZ, stream) as on:
-        dO = on.empty(dZ.shape, dZ.dtype) if dO is None else dO
-        dG = on.empty(dZ.shape, dZ.dtype) if dG is None else dG
-        sums = dweight is not None or dbias is not None
-        ws, wsb = on.workspace(lib().msr_gated_norm_bwd_workspace_bytes(rows, heads, dv) if sums else 0, workspace)
+        if dO is None:
+            dO = on.empty(shape, ty)
+            pdO = dO.data_ptr()
+        if dG is None:
+            dG = on.empty(shape, ty)
+            pdG = dG.data_ptr()
+        need = 0 if pdw is pdc is None else lib().msr_gated_norm_bwd_workspace_bytes(rows, heads, dv)
+        ws, wsb, _keep = on.workspace(need, workspace)
         _check("msr_gated_norm_bwd",
-               lib().msr_gated_norm_bwd(dt, norm, rows, heads, dv, _ptr(dZ), fmt, _ptr(O), _ptr(O_qs), _ptr(G),
-                                        _ptr(G_qs), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(dO),
-                                        _ptr(dG), _ptr(Z), _ptr(dweight), _ptr(dbias), _ptr(ws), wsb, on.handle))
+               lib().msr_gated_norm_bwd(dt, norm, rows, heads, dv, pz, fmt, pO, pOs, pG, pGs, pm, pr, pw, pc, pdO,
+                                        pdG, pZ, pdw, pdc, ws, wsb, on.handle))
     return dO, dG
 
 
 def msr_ckpt_pack(X, fmt=MSR_Q_E4M3, *, q=None, qs=None, stream=None):
     """X [..., cols] in 8 bits.  Returns (q, qs), allocated as msr_ckpt_empty does where not given."""
-    torch = _torch()
+    torch, dev, shape = _torch(), X.device, X.shape
     dt = _dtype_code(X)
     if fmt not in (MSR_Q_E4M3, MSR_Q_I8):
         raise ValueError(f"unknown 8-bit format {fmt}")
-    if X.dim() == 0 or X.shape[-1] % 32:
+    if not shape or shape[-1] % 32:
         raise ValueError("the last dimension must be a multiple of 32")
-    cols, lead = X.shape[-1], X.shape[:-1]
-    qt = torch.int8 if fmt == MSR_Q_I8 else torch.float8_e4m3fn
-    _need("q", q, X.shape, qt, X.device)
-    _need("qs", qs, (*lead, cols // 32), torch.uint8, X.device)
+    cols, lead = shape[-1], shape[:-1]
+    qt, sshape = torch.int8 if fmt == MSR_Q_I8 else torch.float8_e4m3fn, (*lead, cols // 32)
+    pX, pq, ps = _args(dev, ("X", X, shape, X.dtype), ("q", q, shape, qt), ("qs", qs, sshape, torch.uint8))
     with _On(X, stream) as on:
-        q = on.empty(X.shape, qt) if q is None else q
-        qs = on.empty((*lead, cols // 32), torch.uint8) if qs is None else qs
-        _check("msr_ckpt_pack", lib().msr_ckpt_pack(dt, fmt, _rows_of(lead), cols, _ptr(X), _ptr(q), _ptr(qs),
-                                                    on.handle))
+        if q is None:
+            q = on.empty(shape, qt)
+            pq = q.data_ptr()
+        if qs is None:
+            qs = on.empty(sshape, torch.uint8)
+            ps = qs.data_ptr()
+        _check("msr_ckpt_pack", lib().msr_ckpt_pack(dt, fmt, _rows_of(lead), cols, pX, pq, ps, on.handle))
     return q, qs
 
 
 def msr_ckpt_unpack(q, qs, dtype=None, *, mean=None, rstd=None, weight=None, bias=None, out=None, stream=None):
     """The values of (q, qs) in `dtype` (torch.bfloat16 or torch.float32; default: out's, else bfloat16), normalised
     where any of mean, rstd ([...]), weight, bias ([cols], float32) is given.  Returns them."""
-    torch = _torch()
+    torch, dev, shape = _torch(), q.device, q.shape
     f32 = torch.float32
-    fmt = _q_format("q", q, qs, q.shape, q.device)
-    cols, lead = q.shape[-1], q.shape[:-1]
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     if dtype not in (torch.bfloat16, f32):
         raise TypeError(f"unsupported tensor dtype {dtype}; use float32 or bfloat16")
-    _need("out", out, q.shape, dtype, q.device)
-    _need("mean", mean, lead, f32, q.device)
-    _need("rstd", rstd, lead, f32, q.device)
-    _need("weight", weight, (cols,), f32, q.device)
-    _need("bias", bias, (cols,), f32, q.device)
+    fmt, (pq, ps) = _kept(dev, shape, ("q", q, qs))
+    cols, lead = shape[-1], shape[:-1]
+    po, pm, pr, pw, pc = _args(dev, ("out", out, shape, dtype), ("mean", mean, lead, f32), ("rstd", rstd, lead, f32),
+                               ("weight", weight, (cols,), f32), ("bias", bias, (cols,), f32))
     with _On(q, stream) as on:
-        out = on.empty(q.shape, dtype) if out is None else out
+        if out is None:
+            out = on.empty(shape, dtype)
+            po = out.data_ptr()
         _check("msr_ckpt_unpack",
-               lib().msr_ckpt_unpack(MSR_F32 if dtype == f32 else MSR_BF16, fmt, _rows_of(lead), cols, _ptr(q),
-                                     _ptr(qs), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias), _ptr(out),
-                                     on.handle))
+               lib().msr_ckpt_unpack(MSR_F32 if dtype == f32 else MSR_BF16, fmt, _rows_of(lead), cols, pq, ps, pm, pr,
+                                     pw, pc, po, on.handle))
     return out
 
 
@@ -852,27 +869,24 @@ def msr_ckpt_wgrad(q, qs, dY, *, mean=None, rstd=None, weight=None, bias=None, d
                    workspace=None, stream=None):
     """dW = X^T dY (accumulate: dW += X^T dY), X [..., d_in] kept in 8 bits as (q, qs) and normalised as in
     msr_ckpt_unpack; dY: [..., d_out].  Returns dW [d_in, d_out] float32."""
-    f32 = _torch().float32
-    fmt = _q_format("q", q, qs, q.shape, dY.device)
-    d_in, lead = q.shape[-1], q.shape[:-1]
+    f32, dev, shape = _torch().float32, dY.device, q.shape
+    fmt, (pq, ps) = _kept(dev, shape, ("q", q, qs))
+    d_in, lead = shape[-1], shape[:-1]
     d_out = dY.shape[-1]
     dt = _dtype_code(dY)
-    _need("dY", dY, (*lead, d_out), dY.dtype, dY.device)
-    _need("mean", mean, lead, f32, dY.device)
-    _need("rstd", rstd, lead, f32, dY.device)
-    _need("weight", weight, (d_in,), f32, dY.device)
-    _need("bias", bias, (d_in,), f32, dY.device)
-    _need("dW", dW, (d_in, d_out), f32, dY.device)
     if accumulate and dW is None:
         raise ValueError("accumulate needs dW")
-    _need_ws(workspace, dY.device)
-    rows = _rows_of(lead)
+    py, pm, pr, pw, pc, pW = _args(
+        dev, ("dY", dY, (*lead, d_out), dY.dtype), ("mean", mean, lead, f32), ("rstd", rstd, lead, f32),
+        ("weight", weight, (d_in,), f32), ("bias", bias, (d_in,), f32), ("dW", dW, (d_in, d_out), f32))
+    _need_ws(workspace, dev)
+    rows, acc = _rows_of(lead), 1 if accumulate else 0
     with _On(dY, stream) as on:
-        dW = on.empty((d_in, d_out), f32) if dW is None else dW
-        ws, wsb = on.workspace(lib().msr_ckpt_wgrad_workspace_bytes(dt, rows, d_in, d_out, 1 if accumulate else 0),
-                               workspace)
+        if dW is None:
+            dW = on.empty((d_in, d_out), f32)
+            pW = dW.data_ptr()
+        ws, wsb, _keep = on.workspace(lib().msr_ckpt_wgrad_workspace_bytes(dt, rows, d_in, d_out, acc), workspace)
         _check("msr_ckpt_wgrad",
-               lib().msr_ckpt_wgrad(dt, fmt, rows, d_in, d_out, _ptr(q), _ptr(qs), _ptr(mean), _ptr(rstd),
-                                    _ptr(weight), _ptr(bias), _ptr(dY), 1 if accumulate else 0, _ptr(dW), _ptr(ws),
-                                    wsb, on.handle))
+               lib().msr_ckpt_wgrad(dt, fmt, rows, d_in, d_out, pq, ps, pm, pr, pw, pc, py, acc, pW, ws, wsb,
+                                    on.handle))
     return dW

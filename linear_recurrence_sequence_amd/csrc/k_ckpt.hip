@@ -13,17 +13,26 @@ namespace msr {
 
 namespace {
 
-// Units of 8 values, four neighbouring lanes to a group of 32; `units` is a
-// multiple of 4 and so are the thread counts: a quad is on or off as one.
+// A workgroup takes kFlat units of 8 values in a row, 256 at a time; four
+// neighbouring lanes hold a group of 32 (the number of units is a multiple
+// of 4, so a quad is on or off as one).
+constexpr int kFlat = 512;
+
 template <class T, int F>
 __global__ __launch_bounds__(256) void k_ckpt_pack(const T* __restrict__ X, uint8_t* __restrict__ q,
                                                    uint8_t* __restrict__ qs, int64_t units) {
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    Row8<T> r;
-    load_row8(r, X + 8 * u, true);
+  const int64_t at = (int64_t)blockIdx.x * kFlat * 8;
+  const int n = (int)min((int64_t)kFlat, units - (int64_t)blockIdx.x * kFlat);
+  const Win wx(X + at, 8u * (uint32_t)n * (uint32_t)sizeof(T));
+  const HeldWin<T, F> wq(q, qs, at, 8u * (uint32_t)n);
+  Row8<T> r[kFlat / 256];
+#pragma unroll
+  for (int i = 0; i < kFlat / 256; ++i) win_load8(r[i], wx, 8 * (threadIdx.x + 256 * i));
+#pragma unroll
+  for (int i = 0; i < kFlat / 256; ++i) {
     float v[8];
-    unpack_row8(v, r);
-    q_store8<F>(v, q, qs, u);
+    unpack_row8(v, r[i]);
+    q_store8(v, wq, 8 * (threadIdx.x + 256 * i));
   }
 }
 
@@ -44,68 +53,99 @@ struct Norm8 {
 template <class T, int F, bool NORM>
 __global__ __launch_bounds__(256) void k_ckpt_unpack(CkptArgs a, T* __restrict__ X) {
   const int cu = a.cols / 8;
-  const int64_t units = a.rows * cu;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    Held<T, F> h;
-    h.load(a.q, a.qs, u);
+  const int64_t unit0 = (int64_t)blockIdx.x * kFlat, at = unit0 * 8;
+  const int n = (int)min((int64_t)kFlat, a.rows * cu - unit0);
+  const HeldWin<T, F> wq(a.q, a.qs, at, 8u * (uint32_t)n);
+  const Win wx(X + at, 8u * (uint32_t)n * (uint32_t)sizeof(T));
+  Held<T, F> h[kFlat / 256];
+#pragma unroll
+  for (int i = 0; i < kFlat / 256; ++i) h[i].load(wq, 8 * (threadIdx.x + 256 * i));
+#pragma unroll
+  for (int i = 0; i < kFlat / 256; ++i) {
+    const int u = threadIdx.x + 256 * i;
     float v[8];
-    h.values(v);
+    h[i].values(v);
     if constexpr (NORM) {
-      const int64_t row = u / cu;
-      const Norm8 n{a.weight, a.bias};
-      n.apply(v, a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, 8 * (int)(u - row * cu));
+      if (u < n) {
+        const int64_t row = (unit0 + u) / cu;
+        const Norm8 nm{a.weight, a.bias};
+        nm.apply(v, a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, 8 * (int)(unit0 + u - row * cu));
+      }
     }
     Row8<T> r;
     pack_row8(r, v);
-    store_row8(X + 8 * u, r);
+    win_store8(wx, 8 * u, r);
   }
 }
 
-// 64 tokens x 64 columns through LDS: 16 rows at a time are read (8 lanes a
-// row), written to the tile transposed, and each column's 64 tokens stored
-// as one line.
+// tok() tokens (256 bytes of them) x 64 columns through LDS, transposed.  A lane reads 8 columns
+// of two neighbouring tokens and writes each column's pair as one piece;
+// then each column's tokens leave as one line.  A bf16 tile row of 136
+// tokens is 4 banks (mod 64) longer than the last, so that a wave's 32-bit
+// writes (8 columns apart, two tokens apart) spread over the banks.  The
+// workgroups behind the last columns copy the rows of `pad`.
+template <class T>
+constexpr int tok() { return 256 / (int)sizeof(T); }
+
+template <class T>
+__device__ __forceinline__ void put_pair(T* p, float a, float b) {
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
+  else *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+
 template <class T, int F, bool NORM>
-__global__ __launch_bounds__(256) void k_ckpt_unpack_t(CkptArgs a, T* __restrict__ XT, int64_t ld) {
-  constexpr int LD = 64 + 16 / (int)sizeof(T);       // tile row of 64 tokens, padded to keep 16-byte alignment
+__global__ __launch_bounds__(256) void k_ckpt_unpack_t(CkptArgs a, T* __restrict__ XT, int64_t ld, PadRows pad) {
+  constexpr int kTok = tok<T>(), LD = kTok + 16 / (int)sizeof(T);
   __shared__ __attribute__((aligned(16))) T tile[64 * LD];
-  const int64_t t0 = (int64_t)blockIdx.x * 64;
+  if ((int)blockIdx.y >= a.cols / 64) {
+    const int64_t n = pad.rows * (pad.cols / 8), out = pad.rows_out * (pad.cols / 8);
+    const int64_t step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
+    for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + threadIdx.x; u < out;
+         u += step) {
+      Row8<T> r;
+      load_row8(r, (const T*)pad.src + 8 * (u < n ? u : 0), u < n);
+      store_row8((T*)pad.dst + 8 * u, r);
+    }
+    return;
+  }
+  const int64_t t0 = (int64_t)blockIdx.x * kTok;
   const int c0 = blockIdx.y * 64, tid = threadIdx.x;
-  const int cu = a.cols / 8;
+  // the window of these rows (those past the end read as zeros)
+  const uint32_t rows = (uint32_t)max((int64_t)0, min((int64_t)kTok, a.rows - t0));
+  const HeldWin<T, F> wq(a.q, a.qs, t0 * a.cols, rows * (uint32_t)a.cols);
+  const int c = tid & 7;
+  Held<T, F> h[kTok / 64][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (tid >> 3) + 32 * i, c = tid & 7;
-    const int64_t row = t0 + r;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row < a.rows) {
-      Held<T, F> h;
-      h.load(a.q, a.qs, row * cu + c0 / 8 + c);
-      h.values(v);
+  for (int i = 0; i < kTok / 64; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) h[i][j].load(wq, (uint32_t)((2 * (tid >> 3) + 64 * i + j) * a.cols + c0 + 8 * c));
+#pragma unroll
+  for (int i = 0; i < kTok / 64; ++i) {
+    const int r = 2 * (tid >> 3) + 64 * i;
+    float v[2][8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      h[i][j].values(v[j]);
       if constexpr (NORM) {
-        const Norm8 n{a.weight, a.bias};
-        n.apply(v, a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, c0 + 8 * c);
+        const int64_t row = t0 + r + j;
+        if (row < a.rows) {
+          const Norm8 n{a.weight, a.bias};
+          n.apply(v[j], a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, c0 + 8 * c);
+        }
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[(8 * c + e) * LD + r] = (T)v[e];
+    for (int e = 0; e < 8; ++e) put_pair(tile + (8 * c + e) * LD + r, v[0][e], v[1][e]);
   }
   __syncthreads();
+  constexpr int CPC = kTok / 8;                      // 8-token pieces of a column
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int col = (tid >> 3) + 32 * i, t8 = tid & 7;
+  for (int i = 0; i < 64 * CPC / 256; ++i) {
+    const int u = tid + 256 * i, col = u / CPC, t8 = u % CPC;
     Row8<T> r;
     load_row8(r, tile + col * LD + 8 * t8, true);
-    store_row8(XT + (int64_t)(c0 + col) * ld + t0 + 8 * t8, r);
+    if (t0 + 8 * t8 < ld) store_row8(XT + (int64_t)(c0 + col) * ld + t0 + 8 * t8, r);
   }
-}
-
-template <class T>
-__global__ __launch_bounds__(256) void k_pad_rows(const T* __restrict__ src, T* __restrict__ dst, int64_t units,
-                                                  int64_t units_out) {
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (u >= units_out) return;
-  Row8<T> r;
-  load_row8(r, src + 8 * (u < units ? u : 0), u < units);
-  store_row8(dst + 8 * u, r);
 }
 
 __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ part, int parts, float* __restrict__ out,
@@ -121,9 +161,7 @@ __global__ __launch_bounds__(256) void k_sum_parts(const float* __restrict__ par
   *reinterpret_cast<f32x4*>(out + i) = s;
 }
 
-// Workgroups of 256 threads over `units` units: enough to fill the card
-// (2048 threads per CU), each walking with the grid's stride.
-dim3 flat_grid(int64_t units) { return dim3((unsigned)std::min<int64_t>((units + 255) / 256, 256 * 8)); }
+dim3 flat_grid(int64_t units) { return dim3((unsigned)((units + kFlat - 1) / kFlat)); }
 
 }  // namespace
 
@@ -162,31 +200,24 @@ hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipS
   return hipGetLastError();
 }
 
-hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, hipStream_t st) {
+hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, const PadRows& pad,
+                                hipStream_t st) {
   if (a.cols == 0 || ld == 0) return hipSuccess;
-  if (a.cols % 64 || ld % 64 || a.cols / 64 > 65535) return hipErrorInvalidValue;
+  const int kTok = elt == kBF16 ? tok<bf16>() : tok<float>();
+  const int64_t gx = (ld + kTok - 1) / kTok, padded = (pad.rows_out * (pad.cols / 8) + 255) / 256;
+  const int64_t gy = a.cols / 64 + std::min<int64_t>((padded + gx - 1) / gx, 4096);
+  if (a.cols % 64 || ld % 64 || pad.cols % 8 || gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
   TraceScope ts("k_ckpt_unpack_t", st);
-  const dim3 g((unsigned)(ld / 64), a.cols / 64), b(256);
-#define MSR_UNPACK(T, F)                                                                               \
-  if (has_norm(a)) hipLaunchKernelGGL((k_ckpt_unpack_t<T, F, true>), g, b, 0, st, a, (T*)XT, ld);      \
-  else hipLaunchKernelGGL((k_ckpt_unpack_t<T, F, false>), g, b, 0, st, a, (T*)XT, ld);
+  const dim3 g((unsigned)gx, (unsigned)gy), b(256);
+#define MSR_UNPACK(T, F)                                                                                    \
+  if (has_norm(a)) hipLaunchKernelGGL((k_ckpt_unpack_t<T, F, true>), g, b, 0, st, a, (T*)XT, ld, pad);      \
+  else hipLaunchKernelGGL((k_ckpt_unpack_t<T, F, false>), g, b, 0, st, a, (T*)XT, ld, pad);
   if (elt == kBF16) {
     if (fmt == kQE4M3) { MSR_UNPACK(bf16, kQE4M3) } else { MSR_UNPACK(bf16, kQI8) }
   } else {
     if (fmt == kQE4M3) { MSR_UNPACK(float, kQE4M3) } else { MSR_UNPACK(float, kQI8) }
   }
 #undef MSR_UNPACK
-  return hipGetLastError();
-}
-
-hipError_t launch_pad_rows(Elt elt, const void* src, void* dst, int64_t rows, int64_t rows_out, int cols,
-                           hipStream_t st) {
-  const int64_t units = rows * cols / 8, out = rows_out * cols / 8;
-  if (out == 0) return hipSuccess;
-  TraceScope ts("k_pad_rows", st);
-  const dim3 g((unsigned)((out + 255) / 256)), b(256);
-  if (elt == kBF16) hipLaunchKernelGGL((k_pad_rows<bf16>), g, b, 0, st, (const bf16*)src, (bf16*)dst, units, out);
-  else hipLaunchKernelGGL((k_pad_rows<float>), g, b, 0, st, (const float*)src, (float*)dst, units, out);
   return hipGetLastError();
 }
 

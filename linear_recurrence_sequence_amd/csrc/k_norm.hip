@@ -35,25 +35,26 @@ namespace {
 constexpr int kMaxWaves = 16;
 
 // Sum of x over the lanes that share a row: a group of LPR lanes of a wave,
-// or (LPR == 0) the whole workgroup through red, whose two halves take
-// turns: a wave writes a half again only after the barrier of the other
-// half, which every wave reaches after reading the first.
+// or (LPR == 0) the tpr threads (whole waves) of the workgroup's row `rib`,
+// through red, whose two halves take turns: a wave writes a half again only
+// after the barrier of the other half, which every wave reaches after
+// reading the first.
 template <int LPR, int NV>
-__device__ __forceinline__ void row_sums(float (&x)[NV], float (*red)[kMaxWaves][2], int& turn) {
-  static_assert(NV <= 2, "red holds two values per wave");
+__device__ __forceinline__ void row_sums(float (&x)[NV], float (*red)[kMaxWaves][2], int& turn, int rib, int tpr) {
+  static_assert(NV <= 2 && kMaxWaves == 16, "red holds two values per wave, summed by 16 lanes");
 #pragma unroll
   for (int i = 0; i < NV; ++i) x[i] = group_sum<LPR == 0 ? 64 : LPR>(x[i]);
   if constexpr (LPR == 0) {
-    const int nw = blockDim.x >> 6, wave = threadIdx.x >> 6;
+    const int nw = tpr >> 6, w0 = rib * nw, wave = threadIdx.x >> 6, l = threadIdx.x & 15;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int i = 0; i < NV; ++i) red[turn][wave][i] = x[i];
     __syncthreads();
+    const int from = min(w0 + l, kMaxWaves - 1);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float s = 0.f;
-      for (int w = 0; w < nw; ++w) s += red[turn][w][i];
-      x[i] = s;
+      const float v = red[turn][from][i];
+      x[i] = group_sum<16>(l < nw ? v : 0.f);
     }
     turn ^= 1;
   }
@@ -82,216 +83,280 @@ __device__ __forceinline__ float scaled_sum(float alpha, float x, float s, float
   return p + q;
 }
 
+// Walks first, first + stride, ... below end: load(row, at) issues the loads
+// of a turn, step(row, at) computes it, AHEAD turns later.  The turns' rows
+// sit in registers (the loop is unrolled over them, nothing is copied).
+// Turns past the end load nothing (their windows are empty).
+template <int AHEAD, class Row, class Load, class Step>
+__device__ __forceinline__ void pipelined(int64_t first, int64_t end, int64_t stride, Load&& load, Step&& step) {
+  Row q[AHEAD + 1];
+  static_for<AHEAD>([&](auto i) __attribute__((always_inline)) { load(q[i], first + i * stride); });
+  bool more = first < end;
+  while (more) {
+    static_for<AHEAD + 1>([&](auto i) __attribute__((always_inline)) {
+      if (more) {
+        load(q[(i + AHEAD) % (AHEAD + 1)], first + AHEAD * stride);
+        step(q[i], first);
+        first += stride;
+        more = first < end;
+      }
+    });
+  }
+}
+
 // Rows of a row kernel: LPR lanes (a group of a wave) per row, or LPR == 0:
-// the workgroup per row.  A thread holds units u0 + k step, k < VPT, of the
-// row's d / 8.
+// tpr threads (whole waves).  A thread holds units u0 + k step, k < VPT, of
+// the row's d / 8; the workgroup rpb rows side by side, and unit k of a
+// thread lies off(k) elements behind the start of the first of them
+// (outside every window where the row has no such unit).
 template <int LPR>
 struct RowMap {
-  int rpb, rib, u0, step;      // rows per workgroup, row in the workgroup, first unit, unit step
-  __device__ __forceinline__ RowMap() {
-    if constexpr (LPR > 0) {
-      rpb = blockDim.x / LPR;
-      rib = threadIdx.x / LPR;
-      u0 = threadIdx.x % LPR;
-      step = LPR;
-    } else {
-      rpb = 1;
-      rib = 0;
-      u0 = threadIdx.x;
-      step = blockDim.x;
-    }
+  int tpr, rpb, rib, u0, d;         // threads per row, rows, row in the workgroup, first unit, columns
+  __device__ __forceinline__ RowMap(int tpr_, int d_) : d(d_) {
+    tpr = LPR ? LPR : tpr_;
+    rpb = blockDim.x / tpr;
+    rib = threadIdx.x / tpr;
+    if constexpr (LPR == 0) rib = __builtin_amdgcn_readfirstlane(rib);   // whole waves
+    u0 = threadIdx.x - rib * tpr;
+  }
+  __device__ __forceinline__ int unit(int k) const { return u0 + k * tpr; }
+  __device__ __forceinline__ uint32_t off(int k) const {
+    return unit(k) < d / 8 ? (uint32_t)(rib * d + 8 * unit(k)) : kOutside;
   }
 };
 
 template <class T, int LPR, int VPT, int F>
 __global__ __launch_bounds__(LPR ? 256 : 512) void k_resid_norm_fwd(ResidNormArgs a) {
   __shared__ float red[2][kMaxWaves][2];
-  const RowMap<LPR> m;
-  const int units = a.d / 8;
+  const RowMap<LPR> m(blockDim.x, a.d);
   const float inv_d = 1.f / (float)a.d;
   float w[VPT][8], c[VPT][8], s[VPT][8];
-  bool on[VPT];
+  uint32_t off[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int u = m.u0 + k * m.step;
-    on[k] = u < units;
-    load_vec8(w[k], a.weight, u, on[k], 1.f);
-    load_vec8(c[k], a.bias, u, on[k], 0.f);
-    load_vec8(s[k], a.scale, u, on[k], 1.f);
+    off[k] = m.off(k);
+    const bool on = off[k] != kOutside;
+    load_vec8(w[k], a.weight, m.unit(k), on, 1.f);
+    load_vec8(c[k], a.bias, m.unit(k), on, 0.f);
+    // without B its window reads 0, and -1 * 0 = -0 changes no alpha x
+    load_vec8(s[k], a.scale, m.unit(k), on, a.B ? 1.f : -1.f);
   }
+  struct Row {
+    Row8<T> x[VPT], b[VPT];
+  };
+  const int64_t first = (int64_t)blockIdx.x * a.chunk * m.rpb;
+  const int64_t end = min(a.rows, first + (int64_t)a.chunk * m.rpb);
+  // elements of the rows that this turn's windows hold
+  auto span = [&](int64_t row0) { return (uint32_t)(max((int64_t)0, min((int64_t)m.rpb, end - row0)) * a.d); };
+  auto load = [&](Row& q, int64_t row0) __attribute__((always_inline)) {
+    const uint32_t bytes = span(row0) * (uint32_t)sizeof(T);
+    const Win wx((const T*)a.X + row0 * a.d, bytes), wb(a.B ? (const T*)a.B + row0 * a.d : nullptr, bytes);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      win_load8(q.x[k], wx, off[k]);
+      win_load8(q.b[k], wb, off[k]);
+    }
+  };
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * m.rpb + m.rib; row < a.rows; row += (int64_t)gridDim.x * m.rpb) {
-    const int64_t base = row * units;
+  auto step = [&](const Row& cur, int64_t row0) __attribute__((always_inline)) {
+    const int64_t at = row0 * a.d;
+    const uint32_t n = span(row0), bytes = n * (uint32_t)sizeof(T);
+    const Win wh(a.H ? (T*)a.H + at : nullptr, bytes), wy((T*)a.Y + at, bytes);
     float h[VPT][8];
     float sum[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int64_t u = base + m.u0 + k * m.step;
+      float x[8], b[8];
+      unpack_row8(x, cur.x[k]);
+      unpack_row8(b, cur.b[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = 0.f;
-      if (on[k]) {
-        Row8<T> rx, rb;
-        float x[8], b[8];
-        load_row8(rx, (const T*)a.X + 8 * u, true);
-        if (a.B) load_row8(rb, (const T*)a.B + 8 * u, true);
-        unpack_row8(x, rx);
-        if (a.B) {
-          unpack_row8(b, rb);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[k][e] = scaled_sum(a.alpha, x[e], s[k][e], b[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[k][e] = a.alpha * x[e];
-        }
-        Row8<T> rh;
-        pack_row8(rh, h[k]);
-        unpack_row8(h[k], rh);                 // the norm reads the sum as it is held
-        if (a.H) store_row8((T*)a.H + 8 * u, rh);
-        if constexpr (F != kQNone) {
-          q_store8<F>(h[k], a.H_q, a.H_qs, u);
-          if (a.B_q) q_store8<F>(b, a.B_q, a.B_qs, u);
-        }
+      for (int e = 0; e < 8; ++e) h[k][e] = scaled_sum(a.alpha, x[e], s[k][e], b[e]);
+      Row8<T> rh;
+      pack_row8(rh, h[k]);
+      unpack_row8(h[k], rh);                   // the norm reads the sum as it is held
+      win_store8(wh, off[k], rh);
+      if constexpr (F != kQNone) {
+        q_store8(h[k], HeldWin<T, F>(a.H_q, a.H_qs, at, n), off[k]);
+        if (a.B_q) q_store8(b, HeldWin<T, F>(a.B_q, a.B_qs, at, n), off[k]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += h[k][e];
     }
     float mu = 0.f;
     if (a.layer) {
-      row_sums<LPR>(sum, red, turn);
+      row_sums<LPR>(sum, red, turn, 0, m.tpr);
       mu = sum[0] * inv_d;
     }
     float q[1] = {0.f};
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (on[k]) {
+    for (int k = 0; k < VPT; ++k) {
+      const bool on = off[k] != kOutside;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[k][e] -= mu;
-          q[0] += h[k][e] * h[k][e];
-        }
+      for (int e = 0; e < 8; ++e) {
+        h[k][e] -= mu;
+        q[0] += on ? h[k][e] * h[k][e] : 0.f;
       }
-    row_sums<LPR>(q, red, turn);
+    }
+    row_sums<LPR>(q, red, turn, 0, m.tpr);
     const float r = 1.f / sqrtf(q[0] * inv_d + a.eps);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (on[k]) {
-        float y[8];
+    for (int k = 0; k < VPT; ++k) {
+      float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r * w[k][e] + c[k][e];
-        Row8<T> ry;
-        pack_row8(ry, y);
-        store_row8((T*)a.Y + 8 * (base + m.u0 + k * m.step), ry);
-      }
-    if (m.u0 == 0) {
-      if (a.mean) a.mean[row] = mu;
-      if (a.rstd) a.rstd[row] = r;
+      for (int e = 0; e < 8; ++e) y[e] = h[k][e] * r * w[k][e] + c[k][e];
+      Row8<T> ry;
+      pack_row8(ry, y);
+      win_store8(wy, off[k], ry);
     }
-  }
+    const uint32_t so = m.u0 == 0 ? 4u * (uint32_t)m.rib : kOutside, sn = 4u * (uint32_t)(n / (uint32_t)a.d);
+    win_store_f32(Win(a.mean ? a.mean + row0 : nullptr, sn), so, mu);
+    win_store_f32(Win(a.rstd ? a.rstd + row0 : nullptr, sn), so, r);
+  };
+  pipelined<1, Row>(first, end, m.rpb, load, step);
 }
 
+// What the backward reads of one row, as loaded: the loads of the next rows
+// are in flight while this one's sums go round.
+template <class T, int VPT, int F, bool DS>
+struct BwdRow {
+  Row8<T> dy[VPT], dh[VPT];
+  Held<T, F> h[VPT], b[DS ? VPT : 1];
+  float mu, r;
+};
+
+// Threads of the backward's workgroup at most: what the registers hold
+// without spilling.
+template <class T, int LPR, int VPT>
+constexpr int bwd_threads() { return LPR ? 256 : sizeof(T) == 2 && VPT == 1 ? 1024 : 512; }
+
 template <class T, int LPR, int VPT, int F, bool DS>
-__global__ __launch_bounds__(LPR ? 256 : 512) void k_resid_norm_bwd(ResidNormBwdArgs a) {
+__global__ __launch_bounds__((bwd_threads<T, LPR, VPT>())) void k_resid_norm_bwd(ResidNormBwdArgs a) {
+  constexpr int kThreads = bwd_threads<T, LPR, VPT>();
+  constexpr int kUnits = LPR ? LPR : VPT == 1 ? 512 : 1024;     // of a row, at most
   __shared__ float red[2][kMaxWaves][2];
-  __shared__ float comb[LPR ? 256 * 8 : 8];
-  const RowMap<LPR> m;
+  // weight and scale (read each row: two 16-byte reads a unit cost less than
+  // the registers), then the partial sums of the rows side by side
+  __shared__ __attribute__((aligned(16))) float lds[kUnits * 16 > kThreads * 8 ? kUnits * 16 : kThreads * 8];
+  const RowMap<LPR> m(a.tpr, a.d);
   const int units = a.d / 8;
   const float inv_d = 1.f / (float)a.d;
-  float w[VPT][8], s[VPT][8], aw[VPT][8], ac[VPT][8], as[DS ? VPT : 1][8];
-  bool on[VPT];
+  f32x4* const vec = reinterpret_cast<f32x4*>(lds);             // [weight, scale][half][unit]
+  for (int i = threadIdx.x; i < 4 * units; i += blockDim.x) {
+    const int v = i / (2 * units), j = i % (2 * units);          // vector, 16-byte piece
+    const float* p = v ? a.scale : a.weight;
+    vec[v * 2 * kUnits + (j & 1) * kUnits + (j >> 1)] =
+        p ? *reinterpret_cast<const f32x4*>(p + 4 * j) : (f32x4){1.f, 1.f, 1.f, 1.f};
+  }
+  auto vec8 = [&](float* o, int v, int u) {
+    const f32x4 x = vec[v * 2 * kUnits + u], y = vec[v * 2 * kUnits + kUnits + u];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { o[e] = x[e]; o[4 + e] = y[e]; }
+  };
+  __syncthreads();
+  float aw[VPT][8], ac[VPT][8], as[DS ? VPT : 1][8];
+  uint32_t off[VPT];
+  int unit[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int u = m.u0 + k * m.step;
-    on[k] = u < units;
-    load_vec8(w[k], a.weight, u, on[k], 1.f);
-    load_vec8(s[k], a.scale, u, on[k], 1.f);
+    off[k] = m.off(k);
+    unit[k] = min(m.unit(k), units - 1);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       aw[k][e] = ac[k][e] = 0.f;
       if constexpr (DS) as[k][e] = 0.f;
     }
   }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * m.rpb + m.rib; row < a.rows; row += (int64_t)gridDim.x * m.rpb) {
-    const int64_t base = row * units;
-    Row8<T> rdy[VPT], rdh[VPT];
-    Held<T, F> rh[VPT], rb[DS ? VPT : 1];
+  using Row = BwdRow<T, VPT, F, DS>;
+  // elements of the rows that this turn's windows hold; rows past the end and
+  // units past a row read as zeros, r among them, and change nothing
+  auto span = [&](int64_t row0) { return (uint32_t)(max((int64_t)0, min((int64_t)m.rpb, a.rows - row0)) * a.d); };
+  auto load = [&](Row& q, int64_t row0) __attribute__((always_inline)) {
+    const int64_t at = row0 * a.d;
+    const uint32_t n = span(row0), bytes = n * (uint32_t)sizeof(T), sn = 4u * (n / (uint32_t)a.d);
+    const Win wy((const T*)a.dY + at, bytes), wd(a.dH_in ? (const T*)a.dH_in + at : nullptr, bytes);
+    const HeldWin<T, F> wh(a.H, a.H_qs, at, n), wb(DS ? a.B : nullptr, DS ? a.B_qs : nullptr, at, n);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (on[k]) {
-        const int64_t u = base + m.u0 + k * m.step;
-        load_row8(rdy[k], (const T*)a.dY + 8 * u, true);
-        rh[k].load(a.H, a.H_qs, u);
-        if (a.dH_in) load_row8(rdh[k], (const T*)a.dH_in + 8 * u, true);
-        if constexpr (DS) rb[k].load(a.B, a.B_qs, u);
-      }
-    const float mu = a.layer ? a.mean[row] : 0.f, r = a.rstd[row];
+    for (int k = 0; k < VPT; ++k) {
+      win_load8(q.dy[k], wy, off[k]);
+      q.h[k].load(wh, off[k]);
+      win_load8(q.dh[k], wd, off[k]);
+      if constexpr (DS) q.b[k].load(wb, off[k]);
+    }
+    q.mu = win_load_f32(Win(a.layer ? a.mean + row0 : nullptr, sn), 4u * (uint32_t)m.rib);
+    q.r = win_load_f32(Win(a.rstd + row0, sn), 4u * (uint32_t)m.rib);
+  };
+  const float layer = a.layer ? inv_d : 0.f;
+  int turn = 0;
+  auto step = [&](const Row& cur, int64_t row0) __attribute__((always_inline)) {
+    const int64_t at = row0 * a.d;
+    const uint32_t bytes = span(row0) * (uint32_t)sizeof(T);
+    const Win wx((T*)a.dX + at, bytes), wb(a.dB ? (T*)a.dB + at : nullptr, bytes);
+    const float r = cur.r, mur = cur.mu * r;
     float xh[VPT][8], g[VPT][8];
     float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (on[k]) {
-        rh[k].values(xh[k]);
-        unpack_row8(g[k], rdy[k]);
+    for (int k = 0; k < VPT; ++k) {
+      float w[8];
+      vec8(w, 0, unit[k]);
+      cur.h[k].raw(xh[k]);
+      unpack_row8(g[k], cur.dy[k]);
+      const float rs = cur.h[k].scale() * r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xh[k][e] = (xh[k][e] - mu) * r;
-          aw[k][e] += g[k][e] * xh[k][e];
-          ac[k][e] += g[k][e];
-          g[k][e] *= w[k][e];
-          sum[0] += g[k][e];
-          sum[1] += g[k][e] * xh[k][e];
-        }
+      for (int e = 0; e < 8; ++e) {
+        xh[k][e] = xh[k][e] * rs - mur;
+        aw[k][e] += g[k][e] * xh[k][e];
+        ac[k][e] += g[k][e];
+        g[k][e] *= w[e];
+        sum[0] += g[k][e];
+        sum[1] += g[k][e] * xh[k][e];
       }
-    row_sums<LPR>(sum, red, turn);
-    const float m1 = a.layer ? sum[0] * inv_d : 0.f, m2 = sum[1] * inv_d;
+    }
+    row_sums<LPR>(sum, red, turn, m.rib, m.tpr);
+    const float m1 = sum[0] * layer * r, m2 = sum[1] * inv_d * r;
 #pragma unroll
-    for (int k = 0; k < VPT; ++k)
-      if (on[k]) {
-        const int64_t u = base + m.u0 + k * m.step;
-        float dh[8], o[8];
+    for (int k = 0; k < VPT; ++k) {
+      float dh[8], o[8];
+      unpack_row8(dh, cur.dh[k]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dh[e] = 0.f;
-        if (a.dH_in) unpack_row8(dh, rdh[k]);
+      for (int e = 0; e < 8; ++e) dh[e] += r * g[k][e] - (xh[k][e] * m2 + m1);
+      if constexpr (DS) {
+        float b[8];
+        cur.b[k].values(b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dh[e] += r * (g[k][e] - m1 - xh[k][e] * m2);
-        if constexpr (DS) {
-          float b[8];
-          rb[k].values(b);
+        for (int e = 0; e < 8; ++e) as[k][e] += dh[e] * b[e];
+      }
+      Row8<T> ro;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) as[k][e] += dh[e] * b[e];
-        }
-        Row8<T> ro;
+      for (int e = 0; e < 8; ++e) o[e] = a.alpha * dh[e];
+      pack_row8(ro, o);
+      win_store8(wx, off[k], ro);
+      if (a.dB) {
+        float s[8];
+        vec8(s, 1, unit[k]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = a.alpha * dh[e];
+        for (int e = 0; e < 8; ++e) o[e] = s[e] * dh[e];
         pack_row8(ro, o);
-        store_row8((T*)a.dX + 8 * u, ro);
-        if (a.dB) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = s[k][e] * dh[e];
-          pack_row8(ro, o);
-          store_row8((T*)a.dB + 8 * u, ro);
-        }
+        win_store8(wb, off[k], ro);
       }
-  }
-  // this workgroup's partial sums over its rows, one row of d per requested vector
+    }
+  };
+  // every thread of the workgroup takes every turn (row_sums has a barrier)
+  const int64_t stride = (int64_t)gridDim.x * m.rpb;
+  pipelined<1, Row>((int64_t)blockIdx.x * m.rpb, a.rows, stride, load, step);
+  // this workgroup's partial sums over its rows (those side by side added
+  // first), one row of d per requested vector
   auto put = [&](float (&v)[VPT][8], float* dst) {
-    if constexpr (LPR == 0) {
 #pragma unroll
-      for (int k = 0; k < VPT; ++k)
-        if (on[k]) store_vec8(dst + (int64_t)blockIdx.x * a.d + 8 * (m.u0 + k * m.step), v[k]);
-    } else {
+    for (int k = 0; k < VPT; ++k) {
+      __syncthreads();
+      store_vec8(lds + 8 * threadIdx.x, v[k]);
+      __syncthreads();
+      if (m.rib == 0 && off[k] != kOutside) {
+        float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < m.rpb; ++i)
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        __syncthreads();
-        store_vec8(comb + 8 * threadIdx.x, v[k]);
-        __syncthreads();
-        if (m.rib == 0 && on[k]) {
-          float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int i = 0; i < m.rpb; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] += comb[8 * (i * LPR + m.u0) + e];
-          store_vec8(dst + (int64_t)blockIdx.x * a.d + 8 * (m.u0 + k * m.step), t);
-        }
+          for (int e = 0; e < 8; ++e) t[e] += lds[8 * (i * m.tpr + m.u0) + e];
+        store_vec8(dst + (int64_t)blockIdx.x * a.d + 8 * m.unit(k), t);
       }
     }
   };
@@ -347,40 +412,61 @@ struct GateMap {
     col = (int)(i - (int64_t)t0 * units);
     on = t0 < R;
   }
+  // this thread's elements, and the bytes of its statistics, behind those of
+  // the first of the tokens that the grid holds side by side (R units <= 2^20)
+  __device__ __forceinline__ uint32_t off() const { return on ? 8u * (uint32_t)(t0 * units + col) : kOutside; }
+  __device__ __forceinline__ uint32_t stat_off(int heads, int lph) const {
+    return on ? 4u * (uint32_t)(t0 * heads + col / lph) : kOutside;
+  }
 };
 
 __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }
 
+// Elements and statistics that the windows of a turn hold: of the tokens
+// from `first` on, at most R side by side.
+struct GateSpan {
+  int64_t at, sat;
+  uint32_t n, sn;
+  __device__ __forceinline__ GateSpan(int64_t first, int64_t rows, int R, int units, int heads)
+      : at(first * 8 * units), sat(first * heads) {
+    const uint32_t t = (uint32_t)max((int64_t)0, min((int64_t)R, rows - first));
+    n = t * 8u * (uint32_t)units;
+    sn = t * 4u * (uint32_t)heads;
+  }
+};
+
 template <class T, int LPH, int F>
 __global__ __launch_bounds__(256) void k_gated_norm_fwd(GatedNormArgs a) {
   const GateMap m(a.heads, LPH, a.R);
-  if (!m.on) return;
   constexpr float inv_d = 1.f / (8.f * LPH);
   float w[8], c[8];
   load_vec8(w, a.weight, m.col, true, 1.f);
   load_vec8(c, a.bias, m.col, true, 0.f);
-  const int head = m.col / LPH;
-  for (int64_t t = m.t0; t < a.rows; t += a.R) {
-    const int64_t u = t * m.units + m.col;
-    Row8<T> ro, rg;
-    load_row8(ro, (const T*)a.O + 8 * u, true);
-    load_row8(rg, (const T*)a.G + 8 * u, true);
+  const uint32_t off = m.off(), soff = m.col % LPH == 0 ? m.stat_off(a.heads, LPH) : kOutside;
+  struct Row {
+    Row8<T> o, g;
+  };
+  auto load = [&](Row& q, int64_t first) __attribute__((always_inline)) {
+    const GateSpan sp(first, a.rows, a.R, m.units, a.heads);
+    const uint32_t bytes = sp.n * (uint32_t)sizeof(T);
+    win_load8(q.o, Win((const T*)a.O + sp.at, bytes), off);
+    win_load8(q.g, Win((const T*)a.G + sp.at, bytes), off);
+  };
+  auto step = [&](const Row& cur, int64_t first) __attribute__((always_inline)) {
+    const GateSpan sp(first, a.rows, a.R, m.units, a.heads);
     float o[8], g[8];
-    unpack_row8(o, ro);
-    unpack_row8(g, rg);
+    unpack_row8(o, cur.o);
+    unpack_row8(g, cur.g);
     if constexpr (F != kQNone) {
-      q_store8<F>(o, a.O_q, a.O_qs, u);
-      q_store8<F>(g, a.G_q, a.G_qs, u);
+      q_store8(o, HeldWin<T, F>(a.O_q, a.O_qs, sp.at, sp.n), off);
+      q_store8(g, HeldWin<T, F>(a.G_q, a.G_qs, sp.at, sp.n), off);
     }
-    float mu = 0.f;
-    if (a.layer) {
-      float s = 0.f;
+    float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += o[e];
-      mu = group_sum<LPH>(s) * inv_d;
-    }
+    for (int e = 0; e < 8; ++e) s += o[e];
+    const float mu = a.layer ? group_sum<LPH>(s) * inv_d : 0.f;
     float q = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -390,66 +476,90 @@ __global__ __launch_bounds__(256) void k_gated_norm_fwd(GatedNormArgs a) {
     const float r = 1.f / sqrtf(group_sum<LPH>(q) * inv_d + a.eps);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = g[e] * sigmoid_fast(g[e]) * (o[e] * r * w[e] + c[e]);
-    pack_row8(ro, o);
-    store_row8((T*)a.Z + 8 * u, ro);
-    if (m.col % LPH == 0) {
-      if (a.mean) a.mean[t * a.heads + head] = mu;
-      if (a.rstd) a.rstd[t * a.heads + head] = r;
-    }
-  }
+    Row8<T> rz;
+    pack_row8(rz, o);
+    win_store8(Win((T*)a.Z + sp.at, sp.n * (uint32_t)sizeof(T)), off, rz);
+    win_store_f32(Win(a.mean ? a.mean + sp.sat : nullptr, sp.sn), soff, mu);
+    win_store_f32(Win(a.rstd ? a.rstd + sp.sat : nullptr, sp.sn), soff, r);
+  };
+  pipelined<1, Row>(0, a.rows, a.R, load, step);
 }
 
 template <class T, int LPH, int F>
 __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
-  __shared__ float comb[256 * 8];
+  // this thread's weight and bias (read each token: four 16-byte reads cost
+  // less than 16 registers), then the partial sums
+  __shared__ f32x4 vec[4][256];
   const GateMap m(a.heads, LPH, a.R);
-  if (!m.on) return;                           // only where a token spans workgroups: no barrier below then
   constexpr float inv_d = 1.f / (8.f * LPH);
-  float w[8], c[8], aw[8], ac[8];
-  load_vec8(w, a.weight, m.col, true, 1.f);
-  load_vec8(c, a.bias, m.col, true, 0.f);
+  float aw[8], ac[8];
+  {
+    float w[8], c[8];
+    load_vec8(w, a.weight, m.col, true, 1.f);
+    load_vec8(c, a.bias, m.col, true, 0.f);
+    vec[0][threadIdx.x] = (f32x4){w[0], w[1], w[2], w[3]};
+    vec[1][threadIdx.x] = (f32x4){w[4], w[5], w[6], w[7]};
+    vec[2][threadIdx.x] = (f32x4){c[0], c[1], c[2], c[3]};
+    vec[3][threadIdx.x] = (f32x4){c[4], c[5], c[6], c[7]};
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) aw[e] = ac[e] = 0.f;
-  const int head = m.col / LPH;
-  for (int64_t t = m.t0; t < a.rows; t += a.R) {
-    const int64_t u = t * m.units + m.col;
-    Row8<T> rz;
-    Held<T, F> ho, hg;
-    load_row8(rz, (const T*)a.dZ + 8 * u, true);
-    ho.load(a.O, a.O_qs, u);
-    hg.load(a.G, a.G_qs, u);
-    const float mu = a.layer ? a.mean[t * a.heads + head] : 0.f, r = a.rstd[t * a.heads + head];
+  const uint32_t off = m.off(), soff = m.stat_off(a.heads, LPH);
+  struct Row {
+    Row8<T> z;
+    Held<T, F> o, g;
+    float mu, r;
+  };
+  auto load = [&](Row& q, int64_t first) __attribute__((always_inline)) {
+    const GateSpan sp(first, a.rows, a.R, m.units, a.heads);
+    win_load8(q.z, Win((const T*)a.dZ + sp.at, sp.n * (uint32_t)sizeof(T)), off);
+    q.o.load(HeldWin<T, F>(a.O, a.O_qs, sp.at, sp.n), off);
+    q.g.load(HeldWin<T, F>(a.G, a.G_qs, sp.at, sp.n), off);
+    q.mu = win_load_f32(Win(a.layer ? a.mean + sp.sat : nullptr, sp.sn), soff);
+    q.r = win_load_f32(Win(a.rstd + sp.sat, sp.sn), soff);
+  };
+  const float layer = a.layer ? inv_d : 0.f;
+  // tokens past the end read as zeros, dZ among them, and change nothing
+  auto step = [&](const Row& cur, int64_t first) __attribute__((always_inline)) {
+    const GateSpan sp(first, a.rows, a.R, m.units, a.heads);
+    const uint32_t bytes = sp.n * (uint32_t)sizeof(T);
+    const float r = cur.r, mur = cur.mu * r, rs = cur.o.scale() * r;
     float xh[8], g[8], dz[8], z[8];
-    ho.values(xh);
-    hg.values(g);
-    unpack_row8(dz, rz);
+    cur.o.raw(xh);
+    cur.g.values(g);
+    unpack_row8(dz, cur.z);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      xh[e] = (xh[e] - mu) * r;
-      const float n = xh[e] * w[e] + c[e], sg = sigmoid_fast(g[e]), sw = g[e] * sg;
-      z[e] = sw * n;
-      const float dn = dz[e] * sw;
-      g[e] = dz[e] * n * (sg * (1.f + g[e] * (1.f - sg)));
-      aw[e] += dn * xh[e];
-      ac[e] += dn;
-      dz[e] = dn * w[e];
-      s1 += dz[e];
-      s2 += dz[e] * xh[e];
-    }
-    const float m1 = a.layer ? group_sum<LPH>(s1) * inv_d : 0.f, m2 = group_sum<LPH>(s2) * inv_d;
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 w = vec[h][threadIdx.x], c = vec[2 + h][threadIdx.x];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) xh[e] = r * (dz[e] - m1 - xh[e] * m2);
-    Row8<T> ro;
-    pack_row8(ro, xh);
-    store_row8((T*)a.dO + 8 * u, ro);
-    pack_row8(ro, g);
-    store_row8((T*)a.dG + 8 * u, ro);
-    if (a.Z) {
-      pack_row8(ro, z);
-      store_row8((T*)a.Z + 8 * u, ro);
+      for (int j = 0; j < 4; ++j) {
+        const int e = 4 * h + j;
+        xh[e] = xh[e] * rs - mur;
+        const float n = xh[e] * w[j] + c[j], sg = sigmoid_fast(g[e]), sw = g[e] * sg;
+        z[e] = sw * n;
+        const float dn = dz[e] * sw;
+        g[e] = dz[e] * n * (sg + sw * (1.f - sg));
+        aw[e] += dn * xh[e];
+        ac[e] += dn;
+        dz[e] = dn * w[j];
+        s1 += dz[e];
+        s2 += dz[e] * xh[e];
+      }
     }
-  }
+    Row8<T> ro;
+    pack_row8(ro, g);
+    win_store8(Win((T*)a.dG + sp.at, bytes), off, ro);
+    pack_row8(ro, z);
+    win_store8(Win(a.Z ? (T*)a.Z + sp.at : nullptr, bytes), off, ro);
+    const float m1 = group_sum<LPH>(s1) * layer * r, m2 = group_sum<LPH>(s2) * inv_d * r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) xh[e] = r * dz[e] - (xh[e] * m2 + m1);
+    pack_row8(ro, xh);
+    win_store8(Win((T*)a.dO + sp.at, bytes), off, ro);
+  };
+  pipelined<2, Row>(0, a.rows, a.R, load, step);
+  float* const comb = reinterpret_cast<float*>(vec);
   // partial sums: one row of heads * d_v per requested vector and workgroup
   // (its tokens added up first), or per t0 where a token spans workgroups
   const int64_t n = 8 * (int64_t)m.units;
@@ -468,7 +578,7 @@ __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
           for (int e = 0; e < 8; ++e) t[e] += comb[8 * i + e];
         store_vec8(dst, t);
       }
-    } else {
+    } else if (m.on) {
       store_vec8(dst, v);
     }
     dst += P * n;
@@ -478,35 +588,57 @@ __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
 }
 
 // ------------------------------------------------------------- launch shapes
-// Row kernels: lanes per row and units per thread.  Up to 512 columns a row
-// is a group of a wave; beyond, a workgroup.
+// Row kernels: lanes per row (0: whole waves), threads per row and units per
+// thread.  Up to 512 columns a row is a group of a wave; beyond, as many
+// waves as hold it at one unit (two above 4096 columns) a thread.
 struct RowShape {
-  int lpr, vpt, threads, rpb;
+  int lpr, tpr, vpt;
 };
 RowShape row_shape(int d) {
   const int units = d / 8;
-  RowShape s{0, 1, 256, 1};
+  RowShape s{0, 0, 1};
   if (units <= 64) {
     s.lpr = 8;
     while (s.lpr < units) s.lpr *= 2;
-    s.rpb = 256 / s.lpr;
+    s.tpr = s.lpr;
     return s;
   }
   s.vpt = units <= 512 ? 1 : 2;
-  s.threads = ((units + s.vpt - 1) / s.vpt + 63) / 64 * 64;
+  s.tpr = ((units + s.vpt - 1) / s.vpt + 63) / 64 * 64;
   return s;
 }
-// Workgroups of a row kernel: as many as the card keeps in flight at once
-// (2048 threads per CU), and no more than there are rows.
-int row_grid(const RowShape& s, int64_t rows, int per_cu_threads) {
-  const int64_t want = (rows + s.rpb - 1) / s.rpb, cap = (int64_t)256 * std::max(1, per_cu_threads / s.threads);
-  return (int)std::max<int64_t>(1, std::min(want, cap));
+// Threads per CU of the walking kernels.  More loads and stores in flight
+// than these lower the rate HBM reaches for several streams read and written
+// at once: gated_norm backward at 32768 x 16 x 512 from e4m3 (3 read, 3
+// written) took 500 us with 256 threads a CU, 537 with 512 and 590 with 1024;
+// the residual norm's at 32767 x 2560 from int8, whose rows meet at a
+// barrier, 101 us with 960 and 132 with 512; gated_norm forward 38 us at
+// 16384 x 8 x 256 with 2048, 40 with 512 or 1024.
+constexpr int kBwdThreads = 1024, kGateFwdThreads = 2048, kGateBwdThreads = 256;
+// Turns a workgroup of resid_norm forward takes (rows in sequence, so that
+// weight, bias and scale are read once for them) where that leaves kFwdGrid
+// workgroups: 216 us at 32768 x 4096 with 4, 222 with 2, 266 with 1, 227 with 8.
+constexpr int kFwdChunk = 4, kFwdGrid = 2048;
+
+// The backward's workgroup: rows side by side, threads, and workgroups (as
+// many as kBwdThreads per CU make, no more than there are rows).
+struct BwdShape {
+  int rpb, threads, grid;
+};
+BwdShape bwd_shape(Elt elt, const RowShape& s, int64_t rows) {
+  BwdShape b;
+  const int most = s.lpr ? 256 : elt == kBF16 && s.vpt == 1 ? 1024 : 512;
+  b.rpb = std::max(1, most / s.tpr);
+  b.threads = b.rpb * s.tpr;
+  b.grid = (int)std::min<int64_t>((rows + b.rpb - 1) / b.rpb, (int64_t)256 * std::max(1, kBwdThreads / b.threads));
+  return b;
 }
-constexpr int kFwdThreads = 2048, kBwdThreads = 1024;
 
 }  // namespace
 
-int resid_norm_bwd_parts(int64_t rows, int d) { return rows ? row_grid(row_shape(d), rows, kBwdThreads) : 0; }
+int resid_norm_bwd_parts(int64_t rows, int d) {
+  return std::max(bwd_shape(kBF16, row_shape(d), rows).grid, bwd_shape(kF32, row_shape(d), rows).grid);
+}
 
 namespace {
 // Launch of a gated_norm kernel: threads per workgroup, workgroups, tokens
@@ -533,7 +665,7 @@ GateShape gate_shape(int64_t rows, int heads, int d_v, int per_cu_threads) {
 }
 }  // namespace
 
-int gated_norm_bwd_parts(int64_t rows, int heads, int d_v) { return gate_shape(rows, heads, d_v, kBwdThreads).P; }
+int gated_norm_bwd_parts(int64_t rows, int heads, int d_v) { return gate_shape(rows, heads, d_v, kGateBwdThreads).P; }
 
 hipError_t launch_col_sums(const float* part, int P, int n, const ColSumOut& out, int vecs, hipStream_t st) {
   if (vecs == 0) return hipSuccess;
@@ -558,11 +690,15 @@ hipError_t launch_col_sums(const float* part, int P, int n, const ColSumOut& out
     default: CASES(kQNone, CALL)                                                         \
   }
 
-hipError_t launch_resid_norm_fwd(const ResidNormArgs& a, hipStream_t st) {
+hipError_t launch_resid_norm_fwd(const ResidNormArgs& a0, hipStream_t st) {
+  ResidNormArgs a = a0;
   if (a.rows == 0) return hipSuccess;
   TraceScope ts("k_resid_norm_fwd", st);
   const RowShape s = row_shape(a.d);
-  const dim3 grid(row_grid(s, a.rows, kFwdThreads)), block(s.threads);
+  const int rpb = s.lpr ? 256 / s.lpr : 1;
+  a.chunk = (int)std::max<int64_t>(1, std::min<int64_t>(kFwdChunk, a.rows / (rpb * kFwdGrid)));
+  const int64_t per = (int64_t)a.chunk * rpb;
+  const dim3 grid((unsigned)((a.rows + per - 1) / per)), block(rpb * s.tpr);
 #define MSR_F32(L, V, F_) hipLaunchKernelGGL((k_resid_norm_fwd<float, L, V, F_>), grid, block, 0, st, a);
 #define MSR_B16(L, V, F_) hipLaunchKernelGGL((k_resid_norm_fwd<bf16, L, V, F_>), grid, block, 0, st, a);
   if (a.elt == kBF16) { MSR_FMT_CASES(MSR_ROW_CASES, MSR_B16) } else { MSR_FMT_CASES(MSR_ROW_CASES, MSR_F32) }
@@ -575,12 +711,14 @@ hipError_t launch_resid_norm_bwd(const ResidNormBwdArgs& a0, float* dscale, floa
                                  hipStream_t st) {
   ResidNormBwdArgs a = a0;
   const RowShape s = row_shape(a.d);
-  const int P = resid_norm_bwd_parts(a.rows, a.d);
+  const BwdShape bs = bwd_shape(a.elt, s, a.rows);
+  const int P = bs.grid;
+  a.tpr = s.tpr;
   a.sum_w = dweight != nullptr;
   a.sum_c = dbias != nullptr;
   if (a.rows) {
     TraceScope ts("k_resid_norm_bwd", st);
-    const dim3 grid(P), block(s.threads);
+    const dim3 grid(P), block(bs.threads);
 #define MSR_F32(L, V, F_)                                                                       \
   if (dscale) hipLaunchKernelGGL((k_resid_norm_bwd<float, L, V, F_, true>), grid, block, 0, st, a); \
   else hipLaunchKernelGGL((k_resid_norm_bwd<float, L, V, F_, false>), grid, block, 0, st, a);
@@ -613,7 +751,7 @@ hipError_t launch_gated_norm_fwd(const GatedNormArgs& a0, hipStream_t st) {
   GatedNormArgs a = a0;
   if (a.rows == 0) return hipSuccess;
   TraceScope ts("k_gated_norm_fwd", st);
-  const GateShape gs = gate_shape(a.rows, a.heads, a.d_v, kFwdThreads);
+  const GateShape gs = gate_shape(a.rows, a.heads, a.d_v, kGateFwdThreads);
   a.R = gs.R;
   const dim3 grid(gs.grid), block(gs.threads);
 #define MSR_F32(L, F_) hipLaunchKernelGGL((k_gated_norm_fwd<float, L, F_>), grid, block, 0, st, a);
@@ -626,7 +764,7 @@ hipError_t launch_gated_norm_fwd(const GatedNormArgs& a0, hipStream_t st) {
 
 hipError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a0, float* dweight, float* dbias, hipStream_t st) {
   GatedNormBwdArgs a = a0;
-  const GateShape gs = gate_shape(a.rows, a.heads, a.d_v, kBwdThreads);
+  const GateShape gs = gate_shape(a.rows, a.heads, a.d_v, kGateBwdThreads);
   a.R = gs.R;
   a.sum_w = dweight != nullptr;
   a.sum_c = dbias != nullptr;

@@ -203,6 +203,7 @@ struct ResidNormArgs {
   float* mean; float* rstd;                          // [rows], null: not written
   uint8_t* H_q; uint8_t* H_qs;                       // with fmt
   uint8_t* B_q; uint8_t* B_qs;                       // with fmt, null: not written
+  int chunk;                                         // set by the launcher
 };
 hipError_t launch_resid_norm_fwd(const ResidNormArgs& a, hipStream_t st);
 struct ResidNormBwdArgs {
@@ -220,6 +221,7 @@ struct ResidNormBwdArgs {
   void* dX; void* dB;                                // dB null: not written
   float* part;                                       // resid_norm_bwd_parts() rows of d per requested sum
   bool sum_w, sum_c;                                 // set by the launcher
+  int tpr;
 };
 int resid_norm_bwd_parts(int64_t rows, int d);
 // dscale, dweight, dbias null: not computed
@@ -276,13 +278,19 @@ struct CkptArgs {
   const float* mean; const float* rstd; const float* weight; const float* bias;
 };
 hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipStream_t st);
+// Rows of a contiguous [rows, cols] matrix copied and followed by zero rows up
+// to rows_out (0: nothing copied); cols a multiple of 8.
+struct PadRows {
+  const void* src;
+  void* dst;
+  int64_t rows, rows_out;
+  int cols;
+};
 // Their transpose: XT[col][row], row stride ld (a multiple of 64, >= rows),
-// zeros in columns rows .. ld - 1; cols a multiple of 64.
-hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, hipStream_t st);
-// dst[r][c] = src[r][c] for r < rows, 0 for rows <= r < rows_out; contiguous
-// rows of cols (a multiple of 8).
-hipError_t launch_pad_rows(Elt elt, const void* src, void* dst, int64_t rows, int64_t rows_out, int cols,
-                           hipStream_t st);
+// zeros in columns rows .. ld - 1; cols a multiple of 64.  In the same launch
+// the rows of `pad`.
+hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, const PadRows& pad,
+                                hipStream_t st);
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
 hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
 // float32 products of K slices: part[z M N + m N + n] = sum over the K rows

@@ -225,23 +225,31 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 }  // extern "C"
 
 // Weight gradient: X^T (read back, transposed) in the workspace, then the
-// product over the tokens, a multiple of 64 at a time: `splits` slices of
-// `slice` tokens straight from dY, and the `rest` tokens behind them (from a
-// copy of dY padded with zero rows where they are no multiple of 64).  Each
-// slice, and the rest, gives a float32 partial; a single one is dW itself.
+// product over the tokens, a multiple of 64 of them at a time: `splits`
+// slices of `slice` tokens and, where those leave some, the `rest` behind
+// them.  Each slice, and the rest, gives a float32 partial; a single one is
+// dW itself.  dY is read in place; what ends inside 64 tokens comes from a
+// copy padded with zero rows: the rest, or, where dY is small, all of dY, so
+// that the slices take every token and there is one product to launch.
 namespace {
 struct WgradPlan {
-  int64_t ld = 0;                    // row stride of X^T: tokens, rounded up to 64
+  int64_t ld = 0;                    // row stride of X^T: tokens with those padded
   int splits = 0;
   int64_t slice = 0, rest = 0;
   int parts = 0;
-  size_t xt = 0, tail = 0, part = 0, total = 0;
+  int64_t from = 0, copied = 0;      // rows of dY copied: first, and count with padding (0: none)
+  size_t xt = 0, copy = 0, part = 0, total = 0;
 };
+
+// dY up to here is copied whole: 4 us at 4 TB/s for 16 MB, what a second
+// product's launch and ramp cost.
+constexpr size_t kCopyWhole = size_t(8) << 20;
 
 WgradPlan wgrad_plan(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out, bool accumulate) {
   WgradPlan w;
-  const int64_t full = rows / 64;
-  w.ld = ((int64_t)rows + 63) / 64 * 64;
+  const size_t es = size_of(dtype);
+  const int64_t full = rows / 64, slabs = ((int64_t)rows + 63) / 64;
+  const bool whole = rows % 64 && (size_t)rows * d_out * es <= kCopyWhole;
   // Fewest microseconds by a model of the product: rounds of workgroups over
   // the card, each so many 64-token slabs deep, and the partials' traffic.
   // Tile sizes, workgroups per CU and microseconds a slab of the kernel that
@@ -252,25 +260,30 @@ WgradPlan wgrad_plan(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out,
   else if (d_in <= 128) { tm = 128; tn = 64; slab = 0.35; }
   const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn), slots = 256 * per_cu;
   const double part_us = (double)d_in * d_out * 8.0 / 4e6;      // written and read back at 4 TB/s
+  auto product_us = [&](int64_t workgroups, int64_t deep) {
+    return (double)((workgroups + slots - 1) / slots) * ((double)deep * slab + 4.0);
+  };
   double best = 0.0;
-  for (int64_t s = 1; s <= std::min<int64_t>(full, 64); ++s) {
-    const int64_t q = full / s, rest = full - q * s + (rows % 64 ? 1 : 0);
-    const int64_t parts = s + (rest ? 1 : 0);
-    double us = (double)((tiles * s + slots - 1) / slots) * (q * slab + 4.0);
-    if (rest) us += (double)((tiles + slots - 1) / slots) * (rest * slab + 4.0) + 4.0;
-    if (parts > 1) us += parts * part_us + 4.0;
+  for (int64_t s = 1; s <= std::min<int64_t>(whole ? slabs : full, 64); ++s) {
+    const int64_t q = whole ? (slabs + s - 1) / s : full / s, n = whole ? (slabs + q - 1) / q : s;
+    const int64_t rest = whole ? 0 : slabs - q * s, parts = n + (rest ? 1 : 0);
+    double us = product_us(tiles * n, q);
+    if (rest) us += product_us(tiles, rest) + 4.0;
+    if (parts > 1) us += (double)parts * part_us + 4.0;
     if (w.splits == 0 || us < best) {
       best = us;
-      w.splits = (int)s;
+      w.splits = (int)n;
+      w.slice = q * 64;
     }
   }
-  w.slice = w.splits ? full / w.splits * 64 : 0;
-  w.rest = rows - w.slice * w.splits;
+  w.rest = whole ? 0 : rows - w.slice * w.splits;
   w.parts = w.splits + (w.rest ? 1 : 0);
-  const size_t es = size_of(dtype);
+  w.from = whole ? 0 : rows - w.rest;
+  w.copied = whole ? w.slice * w.splits : w.rest % 64 ? (w.rest + 63) / 64 * 64 : 0;
+  w.ld = std::max(slabs * 64, w.slice * w.splits);
   size_t off = 0;
   w.xt = off; off += up256((size_t)d_in * w.ld * es);
-  w.tail = off; off += w.rest % 64 ? up256((size_t)(w.rest + 63) / 64 * 64 * d_out * es) : 0;
+  w.copy = off; off += up256((size_t)w.copied * d_out * es);
   w.part = off; off += w.parts > 1 || accumulate ? up256((size_t)w.parts * d_in * d_out * sizeof(float)) : 0;
   w.total = off;
   return w;
@@ -316,23 +329,19 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
     return accumulate ? ok() : from_hip(launch_sum_parts(nullptr, 0, dW, n, false, st), "msr_ckpt_wgrad");
   char* xt = ws + w.xt;
   float* part = w.parts > 1 || accumulate ? (float*)(ws + w.part) : dW;
-  const CkptArgs a{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias};
-  hipError_t err = launch_ckpt_unpack_t(e, (int)fmt, a, xt, w.ld, st);
+  const char* dy = (const char*)dY;
+  const size_t row_bytes = (size_t)d_out * es;
+  CkptArgs a{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias};
+  const PadRows pad{dy + w.from * row_bytes, ws + w.copy, rows - w.from, w.copied, d_out};
+  hipError_t err = launch_ckpt_unpack_t(e, (int)fmt, a, xt, w.ld, pad, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(read back)");
   if (w.splits)
-    err = launch_gemm_parts(e, xt, w.ld, dY, d_out, part, d_in, d_out, (int)w.slice, w.splits, st);
+    err = launch_gemm_parts(e, xt, w.ld, w.copied && w.from == 0 ? ws + w.copy : dy, d_out, part, d_in, d_out,
+                            (int)w.slice, w.splits, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
   if (w.rest) {
-    const int64_t t0 = rows - w.rest, k = (w.rest + 63) / 64 * 64;
-    const char* b = (const char*)dY + (size_t)t0 * d_out * es;
-    if (w.rest % 64) {
-      char* tail = ws + w.tail;
-      err = launch_pad_rows(e, b, tail, w.rest, k, d_out, st);
-      b = tail;
-    }
-    if (err == hipSuccess)
-      err = launch_gemm_parts(e, xt + (size_t)t0 * es, w.ld, b, d_out, part + (int64_t)w.splits * n, d_in, d_out,
-                              (int)k, 1, st);
+    err = launch_gemm_parts(e, xt + w.from * es, w.ld, w.copied ? ws + w.copy : dy + w.from * row_bytes, d_out,
+                            part + (int64_t)w.splits * n, d_in, d_out, (int)((w.rest + 63) / 64 * 64), 1, st);
     if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(last tokens)");
   }
   if (part != dW) err = launch_sum_parts(part, w.parts, dW, n, accumulate != 0, st);
