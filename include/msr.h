@@ -416,16 +416,18 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 /* Weight gradient of a projection Y = X W whose input was kept in 8 bits:
  *   dW = X^T dY  (accumulate != 0: dW += X^T dY),  float32 [d_in, d_out],
  * X [rows, d_in] read back and normalised as in msr_ckpt_unpack and, where it
- * is normalised, rounded to dtype; dY: [rows, d_out] (dtype).  d_in and
- * d_out multiples of 64, at most 2^20; rows at most 2^22.
- * Workspace: msr_ckpt_wgrad_workspace_bytes(). */
+ * is normalised, rounded to dtype; dY: [rows, d_out] (dtype).  Products are
+ * exact (float32 dtype, normalised: to 2^-25 of each), added in float32.
+ * d_in and d_out multiples of 64, at most 2^20; rows at most 2^20.
+ * Workspace: msr_ckpt_wgrad_workspace_bytes(), normed != 0 where any of mean,
+ * rstd, weight, bias is given. */
 msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in,
                           int32_t d_out, const void* q, const uint8_t* qs, const float* mean,
                           const float* rstd, const float* weight, const float* bias,
                           const void* dY, int32_t accumulate, float* dW, void* workspace,
                           size_t ws_bytes, void* stream);
 size_t msr_ckpt_wgrad_workspace_bytes(msr_dtype dtype, int32_t rows, int32_t d_in,
-                                      int32_t d_out, int32_t accumulate);
+                                      int32_t d_out, int32_t normed, int32_t accumulate);
 
 /* Diagnostics for benchmarks: per-kernel timing with HIP events.
  * msr_trace_enable(1) clears earlier totals and from then on brackets every

@@ -128,7 +128,7 @@ def lib():
         "msr_ckpt_pack": (_I32, [_I32, _I32, _I32, _I32, _P, _P, _P, _P]),
         "msr_ckpt_unpack": (_I32, [_I32, _I32, _I32, _I32] + [_P] * 8),
         "msr_ckpt_wgrad": (_I32, [_I32, _I32, _I32, _I32, _I32] + [_P] * 7 + [_I32, _P, _P, _SZ, _P]),
-        "msr_ckpt_wgrad_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+        "msr_ckpt_wgrad_workspace_bytes": (_SZ, [_I32] * 6),
         "msr_trace_enable": (None, [_I32]),
         "msr_trace_count": (_I32, []),
         "msr_trace_get": (_I32, [_I32, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
@@ -580,7 +580,8 @@ class _On:
         if torch.cuda.current_device() != t.device.index:
             self.guard = torch.cuda.device(t.device)
             self.guard.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the handle without a Stream object (3 us)
+        self.handle = raw(t.device.index) if raw is not None else torch.cuda.current_stream().cuda_stream
         if stream is not None:
             h = stream if isinstance(stream, int) else stream.cuda_stream
             if h != self.handle:
@@ -861,8 +862,8 @@ def msr_ckpt_unpack(q, qs, dtype=None, *, mean=None, rstd=None, weight=None, bia
     return out
 
 
-def msr_ckpt_wgrad_workspace_bytes(dtype: int, rows, d_in, d_out, accumulate=False) -> int:
-    return lib().msr_ckpt_wgrad_workspace_bytes(dtype, rows, d_in, d_out, 1 if accumulate else 0)
+def msr_ckpt_wgrad_workspace_bytes(dtype: int, rows, d_in, d_out, normed=False, accumulate=False) -> int:
+    return lib().msr_ckpt_wgrad_workspace_bytes(dtype, rows, d_in, d_out, 1 if normed else 0, 1 if accumulate else 0)
 
 
 def msr_ckpt_wgrad(q, qs, dY, *, mean=None, rstd=None, weight=None, bias=None, dW=None, accumulate=False,
@@ -885,7 +886,9 @@ def msr_ckpt_wgrad(q, qs, dY, *, mean=None, rstd=None, weight=None, bias=None, d
         if dW is None:
             dW = on.empty((d_in, d_out), f32)
             pW = dW.data_ptr()
-        ws, wsb, _keep = on.workspace(lib().msr_ckpt_wgrad_workspace_bytes(dt, rows, d_in, d_out, acc), workspace)
+        normed = 0 if pm is pr is pw is pc is None else 1
+        ws, wsb, _keep = on.workspace(lib().msr_ckpt_wgrad_workspace_bytes(dt, rows, d_in, d_out, normed, acc),
+                                      workspace)
         _check("msr_ckpt_wgrad",
                lib().msr_ckpt_wgrad(dt, fmt, rows, d_in, d_out, pq, ps, pm, pr, pw, pc, py, acc, pW, ws, wsb,
                                     on.handle))

@@ -858,15 +858,15 @@ hipError_t launch_gemm_splitk(Elt elt, const void* A, int64_t lda, const GemmB& 
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_parts(Elt elt, const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M,
-                             int N, int K, int splits, hipStream_t st) {
+hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
+                             int K, int splits, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
   GemmB b{};
   b.ptr[0] = B; b.ld[0] = ldb;
   b.start[0] = 0; b.start[1] = b.start[2] = b.start[3] = INT32_MAX;
   b.part = part;
   TraceScope ts("k_gemm", st);
-  launch_any(elt, A, lda, b, nullptr, (int64_t)N, M, N, K, splits, st);
+  launch_any(kBF16, A, lda, b, nullptr, (int64_t)N, M, N, K, splits, st);
   return hipGetLastError();
 }
 

@@ -278,24 +278,27 @@ struct CkptArgs {
   const float* mean; const float* rstd; const float* weight; const float* bias;
 };
 hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipStream_t st);
-// Rows of a contiguous [rows, cols] matrix copied and followed by zero rows up
-// to rows_out (0: nothing copied); cols a multiple of 8.
-struct PadRows {
-  const void* src;
-  void* dst;
-  int64_t rows, rows_out;
-  int cols;
+// Operands of a weight gradient X^T dY as bf16 terms (see k_ckpt.hip): terms
+// 1 (bf16 tensors), 3 (float32) or 6 (float32, normalised X).  Token t's term
+// j stands at reduction index ((t / 64) terms + j) 64 + t % 64; indexes past
+// the last token, up to ld (XT) or rows_out (dY), hold zeros.
+// XT[col][index] bf16, row stride ld; a.cols a multiple of 64.
+struct WgradOperands {
+  CkptArgs a;
+  uint16_t* XT;
+  int64_t ld;
+  const void* dY;                    // [rows, cols] of elt, rows of cols (a multiple of 8)
+  int64_t dy_rows, dy_out;           // dy_out: reduction indexes written to dYt (0: dY is not copied)
+  int dy_cols;
+  uint16_t* dYt;                     // [dy_out, dy_cols] bf16
 };
-// Their transpose: XT[col][row], row stride ld (a multiple of 64, >= rows),
-// zeros in columns rows .. ld - 1; cols a multiple of 64.  In the same launch
-// the rows of `pad`.
-hipError_t launch_ckpt_unpack_t(Elt elt, int fmt, const CkptArgs& a, void* XT, int64_t ld, const PadRows& pad,
-                                hipStream_t st);
+hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperands& w, hipStream_t st);
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
 hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
-// float32 products of K slices: part[z M N + m N + n] = sum over the K rows
-// [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K a multiple of 64, N of 8.
-hipError_t launch_gemm_parts(Elt elt, const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M,
-                             int N, int K, int splits, hipStream_t st);
+// float32 products of K slices of bf16 matrices: part[z M N + m N + n] = sum
+// over the K rows [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K a
+// multiple of 64, N of 8.
+hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
+                             int K, int splits, hipStream_t st);
 
 }  // namespace msr

@@ -224,44 +224,44 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 
 }  // extern "C"
 
-// Weight gradient: X^T (read back, transposed) in the workspace, then the
-// product over the tokens, a multiple of 64 of them at a time: `splits`
-// slices of `slice` tokens and, where those leave some, the `rest` behind
-// them.  Each slice, and the rest, gives a float32 partial; a single one is
-// dW itself.  dY is read in place; what ends inside 64 tokens comes from a
-// copy padded with zero rows: the rest, or, where dY is small, all of dY, so
-// that the slices take every token and there is one product to launch.
+// Weight gradient: the operands as bf16 terms in the workspace (X^T always,
+// dY where it needs terms or padding), then the product over the reduction
+// indexes (tokens times terms), 64 of them a slab: `splits` slices of `slice`
+// indexes and, where those leave some, the `rest` behind them.  Each slice,
+// and the rest, gives a float32 partial; a single one is dW itself.  A bf16
+// dY is read in place; what ends inside a slab comes from a copy padded with
+// zero rows: the rest, or, where dY is small, all of dY, so that the slices
+// take every token and there is one product to launch.
 namespace {
 struct WgradPlan {
-  int64_t ld = 0;                    // row stride of X^T: tokens with those padded
+  int64_t ld = 0;                    // row stride of X^T: reduction indexes with those padded
   int splits = 0;
   int64_t slice = 0, rest = 0;
   int parts = 0;
-  int64_t from = 0, copied = 0;      // rows of dY copied: first, and count with padding (0: none)
+  int64_t from = 0, copied = 0;      // dY copied: first token, and reduction indexes written (0: none)
   size_t xt = 0, copy = 0, part = 0, total = 0;
 };
 
-// dY up to here is copied whole: 4 us at 4 TB/s for 16 MB, what a second
-// product's launch and ramp cost.
+// A bf16 dY up to here is copied whole: 4 us at 4 TB/s for 8 MB read and
+// written, what a second product's launch and ramp cost.
 constexpr size_t kCopyWhole = size_t(8) << 20;
 
-WgradPlan wgrad_plan(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out, bool accumulate) {
+WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int32_t d_out, bool accumulate) {
   WgradPlan w;
-  const size_t es = size_of(dtype);
-  const int64_t full = rows / 64, slabs = ((int64_t)rows + 63) / 64;
-  const bool whole = rows % 64 && (size_t)rows * d_out * es <= kCopyWhole;
+  const int64_t full = rows / 64, slabs = ((int64_t)rows + 63) / 64 * terms;
+  const bool whole = dtype == MSR_F32 || (rows % 64 && (size_t)rows * d_out * 2 <= kCopyWhole);
   // Fewest microseconds by a model of the product: rounds of workgroups over
-  // the card, each so many 64-token slabs deep, and the partials' traffic.
-  // Tile sizes, workgroups per CU and microseconds a slab of the kernel that
-  // launch_gemm_parts runs for these sizes.
-  int tm = 256, tn = 256, per_cu = 1;
-  double slab = 1.7;
-  if (dtype == MSR_F32) { tm = tn = 128; per_cu = 2; slab = 8.0; }
-  else if (d_in <= 128) { tm = 128; tn = 64; slab = 0.35; }
-  const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn), slots = 256 * per_cu;
+  // the card (one a CU), each so many slabs deep, and the partials' traffic.
+  // Tile sizes and microseconds a slab of the kernel that launch_gemm_parts
+  // runs for these sizes.  Its choice is within 5 % of the fastest of 1, 2, 3,
+  // 4, 8, 16 and 32 slices on 13 shapes from 64 x 64 to 2048 x 8192 (2048 x
+  // 2048 over 16384 tokens: 165 us with 4, 335 with 1, 389 with 32).
+  const int tm = d_in <= 128 ? 128 : 256, tn = d_in <= 128 ? 64 : 256;
+  const double slab = d_in <= 128 ? 0.35 : 1.7;
+  const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn);
   const double part_us = (double)d_in * d_out * 8.0 / 4e6;      // written and read back at 4 TB/s
   auto product_us = [&](int64_t workgroups, int64_t deep) {
-    return (double)((workgroups + slots - 1) / slots) * ((double)deep * slab + 4.0);
+    return (double)((workgroups + 255) / 256) * ((double)deep * slab + 4.0);
   };
   double best = 0.0;
   for (int64_t s = 1; s <= std::min<int64_t>(whole ? slabs : full, 64); ++s) {
@@ -269,7 +269,7 @@ WgradPlan wgrad_plan(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out,
     const int64_t rest = whole ? 0 : slabs - q * s, parts = n + (rest ? 1 : 0);
     double us = product_us(tiles * n, q);
     if (rest) us += product_us(tiles, rest) + 4.0;
-    if (parts > 1) us += (double)parts * part_us + 4.0;
+    if (parts > 1) us += (double)parts * (part_us + 0.15) + 4.0;
     if (w.splits == 0 || us < best) {
       best = us;
       w.splits = (int)n;
@@ -282,12 +282,15 @@ WgradPlan wgrad_plan(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out,
   w.copied = whole ? w.slice * w.splits : w.rest % 64 ? (w.rest + 63) / 64 * 64 : 0;
   w.ld = std::max(slabs * 64, w.slice * w.splits);
   size_t off = 0;
-  w.xt = off; off += up256((size_t)d_in * w.ld * es);
-  w.copy = off; off += up256((size_t)w.copied * d_out * es);
+  w.xt = off; off += up256((size_t)d_in * w.ld * 2);
+  w.copy = off; off += up256((size_t)w.copied * d_out * 2);
   w.part = off; off += w.parts > 1 || accumulate ? up256((size_t)w.parts * d_in * d_out * sizeof(float)) : 0;
   w.total = off;
   return w;
 }
+
+// bf16 terms of an operand pair (k_ckpt.hip)
+int wgrad_terms(msr_dtype dtype, bool normed) { return dtype == MSR_BF16 ? 1 : normed ? 6 : 3; }
 
 msr_status check_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in, int32_t d_out) {
   msr_status s;
@@ -296,17 +299,18 @@ msr_status check_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in
     return fail(MSR_ERR_SHAPE, "invalid sizes rows=%d d_in=%d d_out=%d", rows, d_in, d_out);
   if (d_in % 64 || d_out % 64 || d_in > (1 << 20) || d_out > (1 << 20))
     return fail(MSR_ERR_UNSUPPORTED, "d_in = %d and d_out = %d must be multiples of 64 up to 2^20", d_in, d_out);
-  if (rows > (1 << 22)) return fail(MSR_ERR_UNSUPPORTED, "rows = %d exceeds 2^22", rows);
+  // a tile's 256 rows of X^T (six terms a token) have 32-bit byte offsets
+  if (rows > (1 << 20)) return fail(MSR_ERR_UNSUPPORTED, "rows = %d exceeds 2^20", rows);
   return MSR_OK;
 }
 }  // namespace
 
 extern "C" {
 
-size_t msr_ckpt_wgrad_workspace_bytes(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out,
+size_t msr_ckpt_wgrad_workspace_bytes(msr_dtype dtype, int32_t rows, int32_t d_in, int32_t d_out, int32_t normed,
                                       int32_t accumulate) {
   if (check_wgrad(dtype, MSR_Q_I8, rows, d_in, d_out)) return 0;
-  return wgrad_plan(dtype, rows, d_in, d_out, accumulate != 0).total;
+  return wgrad_plan(dtype, wgrad_terms(dtype, normed != 0), rows, d_in, d_out, accumulate != 0).total;
 }
 
 msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in, int32_t d_out, const void* q,
@@ -317,30 +321,29 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
   if ((s = check_wgrad(dtype, fmt, rows, d_in, d_out))) return s;
   if (!dW) return fail(MSR_ERR_NULL, "dW must be non-NULL");
   if (rows > 0 && (!q || !qs || !dY)) return fail(MSR_ERR_NULL, "q, qs and dY must be non-NULL");
-  const WgradPlan w = wgrad_plan(dtype, rows, d_in, d_out, accumulate != 0);
+  const int terms = wgrad_terms(dtype, mean || rstd || weight || bias);
+  const WgradPlan w = wgrad_plan(dtype, terms, rows, d_in, d_out, accumulate != 0);
   if ((s = check_ws(workspace, ws_bytes, w.total))) return s;
   if ((s = check_aligned(q, weight, bias, dY, dW, workspace))) return s;
   hipStream_t st = (hipStream_t)stream;
-  const Elt e = elt_of(dtype);
-  const size_t es = size_of(dtype);
   const int64_t n = (int64_t)d_in * d_out;
-  char* ws = (char*)workspace;
   if (rows == 0)
     return accumulate ? ok() : from_hip(launch_sum_parts(nullptr, 0, dW, n, false, st), "msr_ckpt_wgrad");
+  char* ws = (char*)workspace;
   char* xt = ws + w.xt;
+  char* copy = ws + w.copy;
   float* part = w.parts > 1 || accumulate ? (float*)(ws + w.part) : dW;
-  const char* dy = (const char*)dY;
-  const size_t row_bytes = (size_t)d_out * es;
-  CkptArgs a{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias};
-  const PadRows pad{dy + w.from * row_bytes, ws + w.copy, rows - w.from, w.copied, d_out};
-  hipError_t err = launch_ckpt_unpack_t(e, (int)fmt, a, xt, w.ld, pad, st);
-  if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(read back)");
+  const char* from = (const char*)dY + (size_t)w.from * d_out * size_of(dtype);
+  const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)xt, w.ld,
+                          from, rows - w.from, w.copied, d_out, (uint16_t*)copy};
+  hipError_t err = launch_wgrad_operands(elt_of(dtype), (int)fmt, terms, ops, st);
+  if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(operands)");
   if (w.splits)
-    err = launch_gemm_parts(e, xt, w.ld, w.copied && w.from == 0 ? ws + w.copy : dy, d_out, part, d_in, d_out,
-                            (int)w.slice, w.splits, st);
+    err = launch_gemm_parts(xt, w.ld, w.copied && w.from == 0 ? copy : dY, d_out, part, d_in, d_out, (int)w.slice,
+                            w.splits, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
-  if (w.rest) {
-    err = launch_gemm_parts(e, xt + w.from * es, w.ld, w.copied ? ws + w.copy : dy + w.from * row_bytes, d_out,
+  if (w.rest) {                      // bf16 only: one term, w.from is also the reduction index
+    err = launch_gemm_parts(xt + (size_t)w.from * 2, w.ld, w.copied ? copy : from, d_out,
                             part + (int64_t)w.splits * n, d_in, d_out, (int)((w.rest + 63) / 64 * 64), 1, st);
     if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(last tokens)");
   }

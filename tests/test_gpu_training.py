@@ -463,7 +463,7 @@ def test_nothing_is_written_outside(dtype):
                                dbias=out((d,), torch.float32), workspace=ws)
         q, qs = msr.msr_ckpt_pack(X, msr.MSR_Q_I8, q=out((T, d), torch.int8), qs=out((T, d // 32), torch.uint8))
         msr.msr_ckpt_unpack(q, qs, out=out((T, d)))
-        ws = out((msr.msr_ckpt_wgrad_workspace_bytes(code, T, d, d, True),), torch.uint8)
+        ws = out((msr.msr_ckpt_wgrad_workspace_bytes(code, T, d, d, accumulate=True),), torch.uint8)
         dW = out((d, d), torch.float32)
         dW.zero_()
         msr.msr_ckpt_wgrad(q, qs, X, dW=dW, accumulate=True, workspace=ws)
@@ -545,7 +545,7 @@ def _pass_state(T, H, d, seed):
     ws = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")
     o["ws1"] = ws(msr.msr_resid_norm_bwd_workspace_bytes(T, D))
     o["ws2"] = ws(msr.msr_gated_norm_bwd_workspace_bytes(T, H, d))
-    o["ws3"] = ws(msr.msr_ckpt_wgrad_workspace_bytes(1, T, D, D))
+    o["ws3"] = ws(msr.msr_ckpt_wgrad_workspace_bytes(1, T, D, D, normed=True))
     return s, o
 
 

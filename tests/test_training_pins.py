@@ -191,15 +191,16 @@ def test_ckpt_refusals():
         L.msr_ckpt_wgrad(dtype, fmt, rows, i, o, q, FAKE, None, None, None, None, dY, acc, dW, ws, wsb, None)
     assert wg(dtype=4) == 3 and wg(fmt=0) == 3
     assert wg(rows=-1) == 2 and wg(i=0) == 2 and wg(o=-64) == 2
-    assert wg(i=96) == 4 and wg(o=100) == 4 and wg(i=1 << 21) == 4 and wg(rows=(1 << 22) + 1) == 4
+    assert wg(i=96) == 4 and wg(o=100) == 4 and wg(i=1 << 21) == 4 and wg(rows=(1 << 20) + 1) == 4
     assert wg(q=None) == 1 and wg(dY=None) == 1 and wg(dW=None) == 1
     assert wg(ws=None) == 5 and wg(wsb=64) == 5
     assert wg(dW=FAKE + 4) == 4
     assert wg(rows=0, q=None, dY=None, acc=1, ws=None, wsb=0) == 0
     for rows in (1, 63, 64, 65, 4096, 99999):
         for i, o in ((64, 64), (2048, 8192), (192, 320)):
-            a, b = (msr.msr_ckpt_wgrad_workspace_bytes(1, rows, i, o, acc) for acc in (False, True))
-            assert i * (-(-rows // 64) * 64) * 2 <= a <= b
+            for dtype, normed, terms in ((1, 0, 1), (1, 1, 1), (0, 0, 3), (0, 1, 6)):
+                a, b = (msr.msr_ckpt_wgrad_workspace_bytes(dtype, rows, i, o, normed, acc) for acc in (False, True))
+                assert i * (-(-rows // 64) * 64) * 2 * terms <= a <= b
     assert msr.msr_ckpt_wgrad_workspace_bytes(1, 64, 65, 64) == 0
 
 
