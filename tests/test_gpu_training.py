@@ -235,7 +235,7 @@ def test_resid_norm_bwd(T, d, fmt, dtype):
     hq, hs, hv = (H, None, host(H)) if fmt == "none" else keep(H, fmt)
     bq, bs, bv = (b, None, host(b)) if fmt == "none" else keep(b, fmt)
     for layer, opts, alpha in ((True, "hswcB", 1.0), (False, "hsw", 0.6), (True, "", 1.0), (True, "wc", -1.5),
-                               (False, "hsB", 1.0)):
+                               (False, "hsB", 1.0), (True, "hB", 2.0)):
         say("resid bwd", dtype, fmt, T, d, layer, opts, alpha)
         mu, r = (v.astype(np.float32) for v in ot.norm_stats(host(H), layer, 1e-5))
         ds, dw, dc = (empty32(d) if k in opts else None for k in "swc")
@@ -260,7 +260,7 @@ def test_resid_norm_bwd(T, d, fmt, dtype):
 
 # ------------------------------------------------------------- gated norm --
 GATED = [(1, 1, 64), (1, 16, 512), (5, 3, 64), (37, 4, 64), (9, 5, 128), (130, 1, 128), (6, 10, 256), (33, 8, 256),
-         (7, 3, 512), (11, 16, 512), (3000, 2, 64), (700, 7, 128), (260, 128, 64)]
+         (7, 3, 512), (11, 16, 512), (3000, 2, 64), (700, 7, 128), (260, 128, 64), (21, 5, 256), (17, 1, 512), (19, 2, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -346,6 +346,46 @@ def test_wgrad(T, i, o, dtype):
         want = xv.T @ host(dy) + (old if acc else 0.0)
         size = xs.T @ np.abs(host(dy)) + np.abs(old) * acc
         within("dW", dW, want, size + rounded / (E32 * (OPS + T)), "f32", ops=OPS + T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("normed", [False, True])
+def test_wgrad_single_products(dtype, normed):
+    """One token: dW is one product an entry.  float32 dY is taken in three bf16 cuts and a weighted X too, so a
+    missing cut would show as 2^-16 of the product: at most 8 roundings (six products' sum, the weighted x, the
+    result) of 2^-24 each are allowed, for bf16 also the rounding of the weighted x."""
+    msr = _msr()
+    rng = np.random.default_rng(17)
+    i, o = 192, 320
+    x, dy = dev(normal(rng, (1, i), "f32") + 3, dtype), dev(normal(rng, (1, o), "f32") + 3, dtype)
+    w = (1 + 0.3 * rng.standard_normal(i)).astype(np.float32)
+    for fmt in ("e4m3", "i8"):
+        say("single products", dtype, normed, fmt)
+        q, qs, xv = keep(x, fmt)
+        dW = host(msr.msr_ckpt_wgrad(q, qs, dy, weight=f32(w) if normed else None))
+        want = (xv * (w.astype(np.float64) if normed else 1.0)).T @ host(dy)
+        rel = 8 * E32 + (U["bf16"] if normed and dtype == "bf16" else 0.0)
+        assert np.all(np.abs(dW - want) <= rel * np.abs(want)), np.max(np.abs(dW - want) / np.abs(want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wgrad_keeps_bad_values_in_their_row_and_column(dtype):
+    """A group that reads back as NaN spoils the rows of dW of its 32 inputs, an infinity or a NaN in dY the columns of
+    its output; the padding of ragged tokens and of other rows spoils nothing."""
+    msr = _msr()
+    T, i, o = 77, 128, 192
+    rng = np.random.default_rng(19)
+    x, dy = normal(rng, (T, i), dtype), normal(rng, (T, o), dtype)
+    x[76, 40], dy[75, 3], dy[76, 100] = np.nan, np.inf, np.nan
+    say("wgrad with bad values", dtype)
+    q, qs, xv = keep(dev(x, dtype), "e4m3")
+    dW = host(msr.msr_ckpt_wgrad(q, qs, dev(dy, dtype)))
+    bad = np.zeros((i, o), bool)
+    bad[32:64], bad[:, [3, 100]] = True, True
+    assert np.array_equal(~np.isfinite(dW), bad)
+    xg, dg = np.delete(xv, np.arange(32, 64), 1), np.delete(dy.astype(np.float64), [3, 100], 1)
+    got = np.delete(np.delete(dW, np.arange(32, 64), 0), [3, 100], 1)
+    assert np.all(np.abs(got - xg.T @ dg) <= (OPS + T) * E32 * (np.abs(xg).T @ np.abs(dg)))
 
 
 # ----------------------------------------------------- limits and isolation --
@@ -608,6 +648,31 @@ def test_other_stream():
         assert torch.equal(W, wW)
         del junk
     torch.cuda.synchronize()
+
+
+def test_two_streams_at_once():
+    """The same pass on two streams, each with its own tensors and workspaces, enqueued alternately."""
+    import torch
+    msr = _msr()
+    T, H, d = 700, 3, 128
+    want, sets = [], []
+    for seed in (21, 22):
+        s, o = _pass_state(T, H, d, seed)
+        _pass(msr, s, o)
+        torch.cuda.synchronize()
+        want.append({k: o[k].clone() for k in RESULTS})
+        sets.append(_pass_state(T, H, d, seed))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    say("two streams")
+    for _ in range(4):
+        for st, (s, o) in zip(streams, sets):
+            with torch.cuda.stream(st):
+                _pass(msr, s, o)
+    torch.cuda.synchronize()
+    for w, (_, o) in zip(want, sets):
+        for k in RESULTS:
+            assert torch.equal(o[k], w[k]), k
 
 
 @pytest.mark.parametrize("dtype,fmt", [("f32", "none"), ("f32", "i8"), ("bf16", "none"), ("bf16", "e4m3")])
