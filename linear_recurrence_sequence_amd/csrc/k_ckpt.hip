@@ -38,17 +38,24 @@ __global__ __launch_bounds__(256) void k_ckpt_pack(const T* __restrict__ X, uint
   }
 }
 
-// ((x - mean) rstd) weight + bias of 8 neighbouring values
+// ((x - mean) rstd) weight + bias of 8 neighbouring columns, each absent
+// vector's window empty (loads of several rows are in flight together).
 struct Norm8 {
-  const float* weight;
-  const float* bias;
-  __device__ __forceinline__ void apply(float* v, float mu, float r, int col) const {
+  float w[8], c[8];
+  // the columns at element offset `col` of windows of weight and bias
+  __device__ __forceinline__ void load(const CkptArgs& a, const Win& ww, const Win& wc, uint32_t col) {
+    Row8<float> rw, rc;
+    win_load8(rw, ww, col);
+    win_load8(rc, wc, col);
+    unpack_row8(w, rw);
+    unpack_row8(c, rc);
+    if (!a.weight)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = (v[e] - mu) * r;
-      if (weight) v[e] *= weight[col + e];
-      if (bias) v[e] += bias[col + e];
-    }
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+  }
+  __device__ __forceinline__ void apply(float* v, float mu, float r) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (v[e] - mu) * r * w[e] + c[e];
   }
 };
 
@@ -62,21 +69,29 @@ __global__ __launch_bounds__(256) void k_ckpt_unpack(CkptArgs a, T* __restrict__
   Held<T, F> h[kFlat / 256];
 #pragma unroll
   for (int i = 0; i < kFlat / 256; ++i) h[i].load(wq, 8 * (threadIdx.x + 256 * i));
+  Norm8 nm[kFlat / 256];
+  float mu[kFlat / 256], r[kFlat / 256];
+  if constexpr (NORM) {
+    const Win ww(a.weight, 4u * (uint32_t)a.cols), wc(a.bias, 4u * (uint32_t)a.cols);
+    const int64_t row0 = unit0 / cu;                 // of the workgroup's first unit, and that unit's place in it
+    const uint32_t u0 = (uint32_t)(unit0 - row0 * cu), rows = (uint32_t)min((int64_t)(kFlat + 1), a.rows - row0);
+    const Win wm(a.mean ? a.mean + row0 : nullptr, 4u * rows), wr(a.rstd ? a.rstd + row0 : nullptr, 4u * rows);
+#pragma unroll
+    for (int i = 0; i < kFlat / 256; ++i) {
+      const uint32_t u = u0 + threadIdx.x + 256 * i, row = u / (uint32_t)cu;
+      nm[i].load(a, ww, wc, 8 * (u - row * (uint32_t)cu));
+      mu[i] = win_load_f32(wm, 4 * row);
+      r[i] = a.rstd ? win_load_f32(wr, 4 * row) : 1.f;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kFlat / 256; ++i) {
-    const int u = threadIdx.x + 256 * i;
     float v[8];
     h[i].values(v);
-    if constexpr (NORM) {
-      if (u < n) {
-        const int64_t row = (unit0 + u) / cu;
-        const Norm8 nm{a.weight, a.bias};
-        nm.apply(v, a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, 8 * (int)(unit0 + u - row * cu));
-      }
-    }
-    Row8<T> r;
-    pack_row8(r, v);
-    win_store8(wx, 8 * u, r);
+    if constexpr (NORM) nm[i].apply(v, mu[i], r[i]);
+    Row8<T> o;
+    pack_row8(o, v);
+    win_store8(wx, 8 * (threadIdx.x + 256 * i), o);
   }
 }
 
@@ -175,19 +190,37 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) h[i][j].load(wq, (uint32_t)((2 * (tid >> 3) + 64 * i + j) * a.cols + c0 + 8 * c));
   float v[kTok / 64][2][8];
+  if constexpr (NORM) {
+    const Win ww(a.weight ? a.weight + c0 : nullptr, 256), wc(a.bias ? a.bias + c0 : nullptr, 256);
+    const Win wm(a.mean ? a.mean + t0 : nullptr, 4 * rows), wr(a.rstd ? a.rstd + t0 : nullptr, 4 * rows);
+    Norm8 nm;
+    nm.load(a, ww, wc, 8 * c);
+    float mu[kTok / 64][2], r[kTok / 64][2];
 #pragma unroll
-  for (int i = 0; i < kTok / 64; ++i)
+    for (int i = 0; i < kTok / 64; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      h[i][j].values(v[i][j]);
-      if constexpr (NORM) {
-        const int64_t row = t0 + 2 * (tid >> 3) + 64 * i + j;
-        if (row < a.rows) {
-          const Norm8 n{a.weight, a.bias};
-          n.apply(v[i][j], a.mean ? a.mean[row] : 0.f, a.rstd ? a.rstd[row] : 1.f, c0 + 8 * c);
-        }
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t row = 2 * (tid >> 3) + 64 * i + j;
+        mu[i][j] = win_load_f32(wm, 4 * row);
+        r[i][j] = a.rstd ? win_load_f32(wr, 4 * row) : 1.f;
       }
-    }
+#pragma unroll
+    for (int i = 0; i < kTok / 64; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        h[i][j].values(v[i][j]);
+        nm.apply(v[i][j], mu[i][j], r[i][j]);
+        // tokens past the end stay zeros (the bias would not)
+        const bool in = 2 * (tid >> 3) + 64 * i + j < (int)rows;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][j][e] = in ? v[i][j][e] : 0.f;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTok / 64; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) h[i][j].values(v[i][j]);
+  }
 #pragma unroll
   for (int piece = 0; piece < PIECES; ++piece) {
     if (piece) __syncthreads();

@@ -556,7 +556,8 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
 
 // ---------------------------------------------------------------------------
 // k_gemm_sk: bf16 C = A B for at most 128 rows of A (one token per sequence
-// in decode), where the product is a stream of the weights B: 128 x 64
+// in decode), where the product is a stream of the weights B, and for
+// products too small to fill the card with 256 x 256 tiles: 128 x 64
 // output tiles, 64-deep K slabs of both operands copied straight to LDS
 // (direct 16-byte copies) through a ring of 5 slots, 4 slabs (32 KiB of
 // the weight stream) in flight per CU.  8 waves (two per SIMD), wave w:
@@ -596,7 +597,7 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
 
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * BN;
+  const int n0 = blockIdx.x * BN, m0 = blockIdx.y * SC::BM;
   const int kz = blockIdx.z * K;                     // this split's first K row
   const int KT = K / BK;
   // the tile lies inside one weight segment (checked by the launcher)
@@ -605,7 +606,7 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
   const bf16* Bs = reinterpret_cast<const bf16*>(sel(bp.ptr[0], bp.ptr[1], bp.ptr[2], bp.ptr[3]));
   const int64_t ldb = sel(bp.ld[0], bp.ld[1], bp.ld[2], bp.ld[3]);
   const bf16* Bt = Bs + (n0 - sel(bp.start[0], bp.start[1], bp.start[2], bp.start[3])) + (size_t)kz * ldb;
-  const bf16* At = A + kz;
+  const bf16* At = A + (size_t)m0 * lda + kz;
 
   // Per-lane source offsets (elements) of this wave's copies; copy t fills
   // slots 64 (NW t + wave) + lane of the slab (A for t < ACP, then B).
@@ -615,7 +616,7 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
     const int u = 64 * (NW * t + wave) + lane;
     if (t < ACP) {
       const int r = u / 8, c = (u % 8) ^ ((r >> 1) & 7);
-      off[t] = (uint32_t)(min(r, M - 1) * lda + 8 * c);
+      off[t] = (uint32_t)(min(r, M - 1 - m0) * lda + 8 * c);
     } else {
       const int v = u - ASL, r = v / CPR, c = (v % CPR) ^ SC::bsw(r);
       off[t] = (uint32_t)(r * ldb + 8 * c);
@@ -680,7 +681,7 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
     const int n = n0 + (BN / 2) * (wave >> 2) + 32 * tj + lr;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int m = 32 * (wave & 3) + 8 * (r >> 2) + 4 * hh + (r & 3);
+      const int m = m0 + 32 * (wave & 3) + 8 * (r >> 2) + 4 * hh + (r & 3);
       if (m < M) {
         if constexpr (PART) bp.part[(size_t)blockIdx.z * M * ldc + (size_t)m * ldc + n] = acc[tj][r];
         else C[(size_t)m * ldc + n] = (bf16)acc[tj][r];
@@ -859,14 +860,19 @@ hipError_t launch_gemm_splitk(Elt elt, const void* A, int64_t lda, const GemmB& 
 }
 
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int K, int splits, hipStream_t st) {
+                             int K, int splits, bool small_tiles, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
+  if (K % 64 || N % 64 || (M + 127) / 128 > 65535) return hipErrorInvalidValue;
   GemmB b{};
   b.ptr[0] = B; b.ld[0] = ldb;
   b.start[0] = 0; b.start[1] = b.start[2] = b.start[3] = INT32_MAX;
   b.part = part;
   TraceScope ts("k_gemm", st);
-  launch_any(kBF16, A, lda, b, nullptr, (int64_t)N, M, N, K, splits, st);
+  if (small_tiles)
+    hipLaunchKernelGGL((k_gemm_sk<true>), dim3(N / 64, (M + 127) / 128, splits), dim3(512), 0, st, (const bf16*)A, lda,
+                       b, (bf16*)nullptr, (int64_t)N, M, N, K);
+  else
+    launch_dc(dim3((N + 255) / 256, (M + 255) / 256, splits), (const bf16*)A, lda, b, nullptr, (int64_t)N, M, N, K, st);
   return hipGetLastError();
 }
 

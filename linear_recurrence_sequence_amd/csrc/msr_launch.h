@@ -296,9 +296,9 @@ hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperand
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
 hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
 // float32 products of K slices of bf16 matrices: part[z M N + m N + n] = sum
-// over the K rows [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K a
-// multiple of 64, N of 8.
+// over the K rows [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K and N
+// multiples of 64; on 256 x 256 tiles, or small_tiles: 128 x 64.
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int K, int splits, hipStream_t st);
+                             int K, int splits, bool small_tiles, hipStream_t st);
 
 }  // namespace msr

@@ -235,6 +235,7 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 namespace {
 struct WgradPlan {
   int64_t ld = 0;                    // row stride of X^T: reduction indexes with those padded
+  bool small = false;                // the product on 128 x 64 tiles
   int splits = 0;
   int64_t slice = 0, rest = 0;
   int parts = 0;
@@ -251,29 +252,33 @@ WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int
   const int64_t full = rows / 64, slabs = ((int64_t)rows + 63) / 64 * terms;
   const bool whole = dtype == MSR_F32 || (rows % 64 && (size_t)rows * d_out * 2 <= kCopyWhole);
   // Fewest microseconds by a model of the product: rounds of workgroups over
-  // the card (one a CU), each so many slabs deep, and the partials' traffic.
-  // Tile sizes and microseconds a slab of the kernel that launch_gemm_parts
-  // runs for these sizes.  Its choice is within 5 % of the fastest of 1, 2, 3,
-  // 4, 8, 16 and 32 slices on 13 shapes from 64 x 64 to 2048 x 8192 (2048 x
-  // 2048 over 16384 tokens: 165 us with 4, 335 with 1, 389 with 32).
-  const int tm = d_in <= 128 ? 128 : 256, tn = d_in <= 128 ? 64 : 256;
-  const double slab = d_in <= 128 ? 0.35 : 1.7;
-  const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn);
+  // the card (one a CU), each so many slabs deep (1.7 us a slab on 256 x 256
+  // tiles, 0.5 on 128 x 64), and the partials' traffic.  Within 5 % of the
+  // fastest of 1, 2, 3, 4, 8, 16 and 32 slices on 13 shapes from 64 x 64 to
+  // 2048 x 8192 (2048 x 2048 over 16384 tokens: 165 us with 4, 335 with 1, 389
+  // with 32); the small tiles took 28 us against 39 at 2048 x 2048 over 1000
+  // tokens, 43 against 50 at 1024 x 1024 over 8192.
   const double part_us = (double)d_in * d_out * 8.0 / 4e6;      // written and read back at 4 TB/s
-  auto product_us = [&](int64_t workgroups, int64_t deep) {
-    return (double)((workgroups + 255) / 256) * ((double)deep * slab + 4.0);
-  };
   double best = 0.0;
-  for (int64_t s = 1; s <= std::min<int64_t>(whole ? slabs : full, 64); ++s) {
-    const int64_t q = whole ? (slabs + s - 1) / s : full / s, n = whole ? (slabs + q - 1) / q : s;
-    const int64_t rest = whole ? 0 : slabs - q * s, parts = n + (rest ? 1 : 0);
-    double us = product_us(tiles * n, q);
-    if (rest) us += product_us(tiles, rest) + 4.0;
-    if (parts > 1) us += (double)parts * (part_us + 0.15) + 4.0;
-    if (w.splits == 0 || us < best) {
-      best = us;
-      w.splits = (int)n;
-      w.slice = q * 64;
+  for (const bool small : {false, true}) {
+    const int tm = small ? 128 : 256, tn = small ? 64 : 256;
+    const double slab = small ? 0.5 : 1.7;
+    const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn);
+    auto product_us = [&](int64_t workgroups, int64_t deep) {
+      return (double)((workgroups + 255) / 256) * ((double)deep * slab + 4.0);
+    };
+    for (int64_t s = 1; s <= std::min<int64_t>(whole ? slabs : full, 64); ++s) {
+      const int64_t q = whole ? (slabs + s - 1) / s : full / s, n = whole ? (slabs + q - 1) / q : s;
+      const int64_t rest = whole ? 0 : slabs - q * s, parts = n + (rest ? 1 : 0);
+      double us = product_us(tiles * n, q);
+      if (rest) us += product_us(tiles, rest) + 4.0;
+      if (parts > 1) us += (double)parts * (part_us + 0.15) + 4.0;
+      if (w.splits == 0 || us < best) {
+        best = us;
+        w.small = small;
+        w.splits = (int)n;
+        w.slice = q * 64;
+      }
     }
   }
   w.rest = whole ? 0 : rows - w.slice * w.splits;
@@ -340,11 +345,12 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(operands)");
   if (w.splits)
     err = launch_gemm_parts(xt, w.ld, w.copied && w.from == 0 ? copy : dY, d_out, part, d_in, d_out, (int)w.slice,
-                            w.splits, st);
+                            w.splits, w.small, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
   if (w.rest) {                      // bf16 only: one term, w.from is also the reduction index
     err = launch_gemm_parts(xt + (size_t)w.from * 2, w.ld, w.copied ? copy : from, d_out,
-                            part + (int64_t)w.splits * n, d_in, d_out, (int)((w.rest + 63) / 64 * 64), 1, st);
+                            part + (int64_t)w.splits * n, d_in, d_out, (int)((w.rest + 63) / 64 * 64), 1, w.small,
+                            st);
     if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(last tokens)");
   }
   if (part != dW) err = launch_sum_parts(part, w.parts, dW, n, accumulate != 0, st);
