@@ -145,20 +145,15 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
   const int tid = threadIdx.x;
   if ((int)blockIdx.y >= a.cols / 64) {
     // one unit of 8 columns of a token (with those padded) at a time
-    const int cu = w.dy_cols / 8;
-    const int64_t slabs = (w.dy_out + 64 * TERMS - 1) / (64 * TERMS), units = slabs * 64 * cu;
-    const int64_t step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
-    for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + tid; u < units; u += step) {
-      const int64_t row = u / cu;
-      const int c = (int)(u - row * cu);
-      const bool in = row < w.dy_rows;
-      Row8<T> r;
-      load_row8(r, (const T*)w.dY + 8 * (in ? u : 0), in);
-      bf16* const dst = (bf16*)w.dYt + 8 * c;
-      const int64_t k0 = row / 64 * (64 * TERMS) + row % 64;
-      if constexpr (TERMS == 1) {
-        if (k0 < w.dy_out) store_row8(reinterpret_cast<T*>(dst) + k0 * w.dy_cols, r);
-      } else {
+    if constexpr (TERMS > 1) {
+      const int cu = w.dy_cols / 8;
+      const int64_t units = w.ld / TERMS * cu, step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
+      for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + tid; u < units;
+           u += step) {
+        const int64_t row = u / cu;
+        const bool in = row < w.dy_rows;
+        Row8<float> r;
+        load_row8(r, w.dY + 8 * (in ? u : 0), in);
         float v[8], p[3][8];
         unpack_row8(v, r);
 #pragma unroll
@@ -168,11 +163,12 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
 #pragma unroll
           for (int i = 0; i < 3; ++i) p[i][e] = q[i];
         }
+        bf16* const dst = (bf16*)w.dYt + (row / 64 * (64 * TERMS) + row % 64) * w.dy_cols + 8 * (u - row * cu);
 #pragma unroll
         for (int j = 0; j < TERMS; ++j) {
           Row8<bf16> o;
           pack_row8(o, p[dy_piece<TERMS>(j)]);
-          if (k0 + 64 * j < w.dy_out) store_row8(dst + (k0 + 64 * j) * w.dy_cols, o);
+          store_row8(dst + (int64_t)(64 * j) * w.dy_cols, o);
         }
       }
     }
@@ -319,10 +315,10 @@ hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipS
 hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperands& w, hipStream_t st) {
   const CkptArgs& a = w.a;
   if (a.cols == 0 || w.ld == 0) return hipSuccess;
-  const int64_t tokens = (w.ld + 64 * terms - 1) / (64 * terms) * 64, gx = (tokens + kTok - 1) / kTok;
-  const int64_t dy_units = (w.dy_out + 64 * terms - 1) / (64 * terms) * 64 * (w.dy_cols / 8);
+  const int64_t tokens = w.ld / terms, gx = (tokens + kTok - 1) / kTok;
+  const int64_t dy_units = terms > 1 ? tokens * (w.dy_cols / 8) : 0;
   const int64_t gy = a.cols / 64 + std::min<int64_t>(((dy_units + 255) / 256 + gx - 1) / gx, 4096);
-  if (a.cols % 64 || w.ld % 64 || w.dy_cols % 8 || gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
+  if (a.cols % 64 || w.ld % (64 * terms) || w.dy_cols % 8 || gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
   TraceScope ts("k_wgrad_operands", st);
   const dim3 g((unsigned)gx, (unsigned)gy), b(256);
 #define MSR_OPERANDS(T, N, TERMS)                                                                          \

@@ -35,8 +35,22 @@ namespace msr {
 // only the code of the options it uses; kEpiAny checks every option at run
 // time and serves any combination).
 enum : int {
-  kEpiRope = 1, kEpiGelu = 2, kEpiSigmoid = 4, kEpiBias = 8, kEpiResid = 16, kEpiPart = 32, kEpiAny = 63
+  kEpiRope = 1, kEpiGelu = 2, kEpiSigmoid = 4, kEpiBias = 8, kEpiResid = 16, kEpiPart = 32, kEpiAny = 63,
+  // reduction range of a split product (with kEpiPart; GemmB::kextra, kvalid):
+  // slices of K or K + 64, and of those one past the last row of B
+  kUneven = 64, kRagged = 128
 };
+// First K row and K rows of slice z: K each, the first kextra slices 64 more.
+template <int OPT>
+__device__ __forceinline__ void split_range(const GemmB& bp, int K, int& kz, int& rows) {
+  const int z = blockIdx.z;
+  kz = z * K;
+  rows = K;
+  if constexpr ((OPT & kUneven) != 0) {
+    kz += 64 * min(z, bp.kextra);
+    rows += z < bp.kextra ? 64 : 0;
+  }
+}
 
 // Epilogue through LDS: each wave stages 32 of its rows at a time in
 // float32, then every lane takes 8 consecutive columns of one row -- a
@@ -419,7 +433,9 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int KT = K / BK;
+  int kz, krows;                                     // split-K: first K row of this workgroup, and its rows
+  split_range<EPI>(bp, K, kz, krows);
+  const int KT = krows / BK;
   // tile order: as k_gemm (contiguous tile ranges per XCD), 4 tile-rows at
   // a time (4, 2, 1, 8 and 16 measured on the projection shapes: 4 fastest)
   const int Mt = gridDim.y, Nt = gridDim.x, total = Mt * Nt;
@@ -435,7 +451,6 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   // first half of the waves the A rows, the second half the B k-rows (of
   // the weight segment that holds the tile).  Rows past M and columns past
   // N are clamped: they feed outputs that are never stored.
-  const int kz = blockIdx.z * K;                     // split-K: first K row of this workgroup
   const bool isA = wave < NW / 2;                    // wave-uniform
   const int sg0 = (n0 >= bp.start[1]) + (n0 >= bp.start[2]) + (n0 >= bp.start[3]);
   const bf16* bseg = reinterpret_cast<const bf16*>(sg0 == 0 ? bp.ptr[0] : sg0 == 1 ? bp.ptr[1] : sg0 == 2 ? bp.ptr[2]
@@ -461,8 +476,30 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   // copy t of slab kt into its ring slot; slabs past the end copy the last
   // slab again (into a slot no slab still needs), so that every step issues
   // the same copies and the waits are fixed
+  // Ragged: the slab that holds B's last row reads the rows past it as that
+  // row, and so does a slab behind it, from that slab again (A holds zeros
+  // there).  Selected without a branch, so that the copies stay between the
+  // MFMAs.
+  constexpr bool RAG = (EPI & kRagged) != 0;
+  const int tail0 = RAG ? (bp.kvalid - 1) / BK * BK : 0;   // first row of that slab
+  uint32_t toff[RAG ? CPW : 1];
+  if constexpr (RAG) {
+#pragma unroll
+    for (int t = 0; t < CPW; ++t) {
+      const int kr = (((wave % (NW / 2)) * CPW + t) * 64 + lane) >> 5;
+      toff[t] = off[t] - (uint32_t)((kr - min(kr, bp.kvalid - 1 - tail0)) * ldb * 2);
+    }
+  }
   auto issue = [&](int kt, int t) {
-    copy16_to_lds(src + min(kt, KT - 1) * kstep, off[t], lbase + (uint32_t)((kt % NS) * SLOTS * 16 + t * 1024));
+    const int kk = min(kt, KT - 1);
+    const bf16* base = src + kk * kstep;
+    uint32_t o = off[t];
+    if constexpr (RAG) {
+      const bool tail = !isA && kz + kk * BK >= tail0;
+      base = tail ? src + (tail0 - kz) * ldb : base;
+      o = tail ? toff[t] : o;
+    }
+    copy16_to_lds(base, o, lbase + (uint32_t)((kt % NS) * SLOTS * 16 + t * 1024));
   };
 
   // Fragments: lane lr reads row lr of a 32-row block, chunk 2 s + hh of
@@ -587,7 +624,7 @@ struct SkCfg {
   static __device__ __forceinline__ int bsw(int r) { return 4 * ((r >> 1) & 1); }
 };
 
-template <bool PART>
+template <bool PART, int OPT = 0>
 __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int64_t lda, GemmB bp,
                                                  bf16* __restrict__ C, int64_t ldc, int M, int N, int K) {
   using SC = SkCfg;
@@ -598,8 +635,9 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * BN, m0 = blockIdx.y * SC::BM;
-  const int kz = blockIdx.z * K;                     // this split's first K row
-  const int KT = K / BK;
+  int kz, krows;                                     // this split's first K row, and its rows
+  split_range<OPT>(bp, K, kz, krows);
+  const int KT = krows / BK;
   // the tile lies inside one weight segment (checked by the launcher)
   const int sg = (n0 >= bp.start[1]) + (n0 >= bp.start[2]) + (n0 >= bp.start[3]);
   auto sel = [&](auto a0, auto a1, auto a2, auto a3) { return sg == 0 ? a0 : (sg == 1 ? a1 : (sg == 2 ? a2 : a3)); };
@@ -622,6 +660,14 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
       off[t] = (uint32_t)(r * ldb + 8 * c);
     }
   }
+  uint32_t toff[(OPT & kRagged) != 0 ? CPW - ACP : 1];
+  if constexpr ((OPT & kRagged) != 0) {
+#pragma unroll
+    for (int t = ACP; t < CPW; ++t) {
+      const int r = (64 * (NW * t + wave) + lane - ASL) / CPR;
+      toff[t - ACP] = off[t] - (uint32_t)((r - min(r, (bp.kvalid - 1) % BK)) * ldb);
+    }
+  }
   lds_char* const lds = (lds_char*)smem;
   // copies of slab j into its slot (slabs past the last re-copy the last
   // one, into a slot no wave reads again, so that every slab issues CPW
@@ -631,9 +677,15 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
     const uint32_t dst = (uint32_t)(uintptr_t)(lds + (j % NS) * STG) + wave * 1024;
     const bf16* a = At + (size_t)jj * BK;
     const bf16* b = Bt + (size_t)jj * BK * ldb;
+    // the slab that holds B's last row (the last one) reads the rows past it as that row (A holds zeros there)
+    const bool tail = (OPT & kRagged) != 0 && kz + (jj + 1) * BK > bp.kvalid;
 #pragma unroll
-    for (int t = 0; t < CPW; ++t)
-      copy16_to_lds(t < ACP ? a : b, 2 * off[t], __builtin_amdgcn_readfirstlane(dst + t * NW * 1024));
+    for (int t = 0; t < CPW; ++t) {
+      uint32_t o = off[t];
+      if constexpr ((OPT & kRagged) != 0)
+        if (t >= ACP) o = tail ? toff[t - ACP] : o;
+      copy16_to_lds(t < ACP ? a : b, 2 * o, __builtin_amdgcn_readfirstlane(dst + t * NW * 1024));
+    }
   };
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) issue(j);
@@ -860,19 +912,36 @@ hipError_t launch_gemm_splitk(Elt elt, const void* A, int64_t lda, const GemmB& 
 }
 
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int K, int splits, bool small_tiles, hipStream_t st) {
+                             int slabs, int rows, int splits, bool small_tiles, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
-  if (K % 64 || N % 64 || (M + 127) / 128 > 65535) return hipErrorInvalidValue;
+  if (N % 64 || (M + 127) / 128 > 65535 || splits < 1 || splits > slabs || rows <= 64 * (slabs - 1) ||
+      rows > 64 * slabs)
+    return hipErrorInvalidValue;
   GemmB b{};
   b.ptr[0] = B; b.ld[0] = ldb;
   b.start[0] = 0; b.start[1] = b.start[2] = b.start[3] = INT32_MAX;
   b.part = part;
+  b.kextra = slabs % splits;
+  b.kvalid = rows;
+  const int K = slabs / splits * 64;
   TraceScope ts("k_gemm", st);
-  if (small_tiles)
-    hipLaunchKernelGGL((k_gemm_sk<true>), dim3(N / 64, (M + 127) / 128, splits), dim3(512), 0, st, (const bf16*)A, lda,
-                       b, (bf16*)nullptr, (int64_t)N, M, N, K);
-  else
-    launch_dc(dim3((N + 255) / 256, (M + 255) / 256, splits), (const bf16*)A, lda, b, nullptr, (int64_t)N, M, N, K, st);
+  const bf16* a = (const bf16*)A;
+  bf16* const none = nullptr;
+  const dim3 block(512);
+  if (small_tiles) {
+    const dim3 grid(N / 64, (M + 127) / 128, splits);
+    if (rows < 64 * slabs)
+      hipLaunchKernelGGL((k_gemm_sk<true, kUneven | kRagged>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
+    else
+      hipLaunchKernelGGL((k_gemm_sk<true, kUneven>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
+    return hipGetLastError();
+  }
+  const dim3 grid((N + 255) / 256, (M + 255) / 256, splits);
+#define MSR_PARTS(OPT)                                                                                              \
+  if (N <= 8192) hipLaunchKernelGGL((k_gemm_dc<OPT, 4, 8, 1>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K); \
+  else hipLaunchKernelGGL((k_gemm_dc<OPT, 4, 8, 0>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
+  if (rows < 64 * slabs) { MSR_PARTS(kEpiPart | kUneven | kRagged) } else { MSR_PARTS(kEpiPart | kUneven) }
+#undef MSR_PARTS
   return hipGetLastError();
 }
 

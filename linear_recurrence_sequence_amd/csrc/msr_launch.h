@@ -161,6 +161,9 @@ struct GemmB {
   // [z K_s, (z + 1) K_s) and stores float32 partials to part + z M N (no
   // rotation); launch_gemm_splitk adds them up.
   float* part;
+  // launch_gemm_parts: the first kextra slices take 64 more K rows, and B has
+  // kvalid rows
+  int kextra, kvalid;
   // epilogue: C = act(A B + bias) + resid, act = gelu when act == 1 and
   // sigmoid when act == 2 (after any rotation), bias[s] a float32 vector
   // over segment s's columns (nullable), resid an [M, N] matrix with row
@@ -281,24 +284,28 @@ hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipS
 // Operands of a weight gradient X^T dY as bf16 terms (see k_ckpt.hip): terms
 // 1 (bf16 tensors), 3 (float32) or 6 (float32, normalised X).  Token t's term
 // j stands at reduction index ((t / 64) terms + j) 64 + t % 64; indexes past
-// the last token, up to ld (XT) or rows_out (dY), hold zeros.
+// the last token, up to ld = the tokens rounded up to 64, times terms, hold
+// zeros.
 // XT[col][index] bf16, row stride ld; a.cols a multiple of 64.
 struct WgradOperands {
   CkptArgs a;
   uint16_t* XT;
   int64_t ld;
-  const void* dY;                    // [rows, cols] of elt, rows of cols (a multiple of 8)
-  int64_t dy_rows, dy_out;           // dy_out: reduction indexes written to dYt (0: dY is not copied)
+  const float* dY;                   // terms > 1: [rows, dy_cols], cut into terms; dy_cols a multiple of 8
+  int64_t dy_rows;
   int dy_cols;
-  uint16_t* dYt;                     // [dy_out, dy_cols] bf16
+  uint16_t* dYt;                     // [ld, dy_cols] bf16
 };
 hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperands& w, hipStream_t st);
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
 hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
-// float32 products of K slices of bf16 matrices: part[z M N + m N + n] = sum
-// over the K rows [z K, (z + 1) K) of A[m][k] B[k][n], z < splits; K and N
-// multiples of 64; on 256 x 256 tiles, or small_tiles: 128 x 64.
+// float32 products of K slices of bf16 matrices: the 64 slabs rows of K are
+// cut into `splits` slices of whole slabs (the first slabs % splits one slab
+// longer), slice z's product of A[m][k] B[k][n] in part[z M N + m N + n].  B
+// has `rows` rows, 64 (slabs - 1) < rows <= 64 slabs; A's columns past them
+// hold zeros (what is read as B's rows there is its last one).  N a
+// multiple of 64; on 256 x 256 tiles, or small_tiles: 128 x 64.
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int K, int splits, bool small_tiles, hipStream_t st);
+                             int slabs, int rows, int splits, bool small_tiles, hipStream_t st);
 
 }  // namespace msr

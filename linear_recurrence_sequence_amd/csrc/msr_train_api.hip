@@ -225,32 +225,21 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 }  // extern "C"
 
 // Weight gradient: the operands as bf16 terms in the workspace (X^T always,
-// dY where it needs terms or padding), then the product over the reduction
-// indexes (tokens times terms), 64 of them a slab: `splits` slices of `slice`
-// indexes and, where those leave some, the `rest` behind them.  Each slice,
-// and the rest, gives a float32 partial; a single one is dW itself.  A bf16
-// dY is read in place; what ends inside a slab comes from a copy padded with
-// zero rows: the rest, or, where dY is small, all of dY, so that the slices
-// take every token and there is one product to launch.
+// dY where it is float32; a bf16 dY is read in place), then the product over
+// the reduction indexes (tokens times terms), 64 of them a slab, in `splits`
+// slices of whole slabs.  Each slice gives a float32 partial; a single one is
+// dW itself.
 namespace {
 struct WgradPlan {
-  int64_t ld = 0;                    // row stride of X^T: reduction indexes with those padded
+  int64_t slabs = 0;
   bool small = false;                // the product on 128 x 64 tiles
   int splits = 0;
-  int64_t slice = 0, rest = 0;
-  int parts = 0;
-  int64_t from = 0, copied = 0;      // dY copied: first token, and reduction indexes written (0: none)
-  size_t xt = 0, copy = 0, part = 0, total = 0;
+  size_t xt = 0, dyt = 0, part = 0, total = 0;
 };
-
-// A bf16 dY up to here is copied whole: 4 us at 4 TB/s for 8 MB read and
-// written, what a second product's launch and ramp cost.
-constexpr size_t kCopyWhole = size_t(8) << 20;
 
 WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int32_t d_out, bool accumulate) {
   WgradPlan w;
-  const int64_t full = rows / 64, slabs = ((int64_t)rows + 63) / 64 * terms;
-  const bool whole = dtype == MSR_F32 || (rows % 64 && (size_t)rows * d_out * 2 <= kCopyWhole);
+  w.slabs = ((int64_t)rows + 63) / 64 * terms;
   // Fewest microseconds by a model of the product: rounds of workgroups over
   // the card (one a CU), each so many slabs deep (1.7 us a slab on 256 x 256
   // tiles, 0.5 on 128 x 64), and the partials' traffic.  Within 5 % of the
@@ -264,32 +253,20 @@ WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int
     const int tm = small ? 128 : 256, tn = small ? 64 : 256;
     const double slab = small ? 0.5 : 1.7;
     const int64_t tiles = (int64_t)((d_in + tm - 1) / tm) * ((d_out + tn - 1) / tn);
-    auto product_us = [&](int64_t workgroups, int64_t deep) {
-      return (double)((workgroups + 255) / 256) * ((double)deep * slab + 4.0);
-    };
-    for (int64_t s = 1; s <= std::min<int64_t>(whole ? slabs : full, 64); ++s) {
-      const int64_t q = whole ? (slabs + s - 1) / s : full / s, n = whole ? (slabs + q - 1) / q : s;
-      const int64_t rest = whole ? 0 : slabs - q * s, parts = n + (rest ? 1 : 0);
-      double us = product_us(tiles * n, q);
-      if (rest) us += product_us(tiles, rest) + 4.0;
-      if (parts > 1) us += (double)parts * (part_us + 0.15) + 4.0;
+    for (int64_t s = 1; s <= std::min<int64_t>(w.slabs, 64); ++s) {
+      double us = (double)((tiles * s + 255) / 256) * ((double)((w.slabs + s - 1) / s) * slab + 4.0);
+      if (s > 1) us += (double)s * (part_us + 0.15) + 4.0;
       if (w.splits == 0 || us < best) {
         best = us;
         w.small = small;
-        w.splits = (int)n;
-        w.slice = q * 64;
+        w.splits = (int)s;
       }
     }
   }
-  w.rest = whole ? 0 : rows - w.slice * w.splits;
-  w.parts = w.splits + (w.rest ? 1 : 0);
-  w.from = whole ? 0 : rows - w.rest;
-  w.copied = whole ? w.slice * w.splits : w.rest % 64 ? (w.rest + 63) / 64 * 64 : 0;
-  w.ld = std::max(slabs * 64, w.slice * w.splits);
   size_t off = 0;
-  w.xt = off; off += up256((size_t)d_in * w.ld * 2);
-  w.copy = off; off += up256((size_t)w.copied * d_out * 2);
-  w.part = off; off += w.parts > 1 || accumulate ? up256((size_t)w.parts * d_in * d_out * sizeof(float)) : 0;
+  w.xt = off; off += up256((size_t)d_in * w.slabs * 64 * 2);
+  w.dyt = off; off += dtype == MSR_F32 ? up256((size_t)w.slabs * 64 * d_out * 2) : 0;
+  w.part = off; off += w.splits > 1 || accumulate ? up256((size_t)w.splits * d_in * d_out * sizeof(float)) : 0;
   w.total = off;
   return w;
 }
@@ -335,25 +312,17 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
   if (rows == 0)
     return accumulate ? ok() : from_hip(launch_sum_parts(nullptr, 0, dW, n, false, st), "msr_ckpt_wgrad");
   char* ws = (char*)workspace;
-  char* xt = ws + w.xt;
-  char* copy = ws + w.copy;
-  float* part = w.parts > 1 || accumulate ? (float*)(ws + w.part) : dW;
-  const char* from = (const char*)dY + (size_t)w.from * d_out * size_of(dtype);
-  const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)xt, w.ld,
-                          from, rows - w.from, w.copied, d_out, (uint16_t*)copy};
+  const bool f32 = dtype == MSR_F32;
+  float* part = w.splits > 1 || accumulate ? (float*)(ws + w.part) : dW;
+  const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)(ws + w.xt),
+                          w.slabs * 64, f32 ? (const float*)dY : nullptr, rows, d_out,
+                          f32 ? (uint16_t*)(ws + w.dyt) : nullptr};
   hipError_t err = launch_wgrad_operands(elt_of(dtype), (int)fmt, terms, ops, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(operands)");
-  if (w.splits)
-    err = launch_gemm_parts(xt, w.ld, w.copied && w.from == 0 ? copy : dY, d_out, part, d_in, d_out, (int)w.slice,
-                            w.splits, w.small, st);
+  err = launch_gemm_parts(ws + w.xt, w.slabs * 64, f32 ? (const void*)(ws + w.dyt) : dY, d_out, part, d_in, d_out,
+                          (int)w.slabs, f32 ? (int)w.slabs * 64 : rows, w.splits, w.small, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
-  if (w.rest) {                      // bf16 only: one term, w.from is also the reduction index
-    err = launch_gemm_parts(xt + (size_t)w.from * 2, w.ld, w.copied ? copy : from, d_out,
-                            part + (int64_t)w.splits * n, d_in, d_out, (int)((w.rest + 63) / 64 * 64), 1, w.small,
-                            st);
-    if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(last tokens)");
-  }
-  if (part != dW) err = launch_sum_parts(part, w.parts, dW, n, accumulate != 0, st);
+  if (part != dW) err = launch_sum_parts(part, w.splits, dW, n, accumulate != 0, st);
   return from_hip(err, "msr_ckpt_wgrad(sum)");
 }
 

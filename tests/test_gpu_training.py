@@ -348,6 +348,26 @@ def test_wgrad(T, i, o, dtype):
         within("dW", dW, want, size + rounded / (E32 * (OPS + T)), "f32", ops=OPS + T)
 
 
+@pytest.mark.parametrize("T", [2048, 2049, 3000, 3105])
+def test_wgrad_on_large_tiles(T):
+    """bf16 on the 256 x 256 tiles: whole slabs, one token in the last slab, slices of unequal length, a last slab
+    half full.  The same bound as above; the reference products in float64 (torch, on the GPU)."""
+    import torch
+    msr = _msr()
+    rng = np.random.default_rng(T)
+    i, o = 2048, 4096
+    x, dy = dev(normal(rng, (T, i), "bf16"), "bf16"), dev(normal(rng, (T, o), "bf16", 0.3), "bf16")
+    say("wgrad on large tiles", T)
+    q, qs = msr.msr_ckpt_pack(x, msr.MSR_Q_I8)
+    dW = msr.msr_ckpt_wgrad(q, qs, dy)
+    xv = msr.msr_ckpt_unpack(q, qs, torch.float32).double().t().contiguous()
+    dyd = dy.double()
+    err, size = (dW.double() - xv @ dyd).abs(), xv.abs() @ dyd.abs()
+    assert bool((err <= (OPS + T) * E32 * size).all()), float((err / size).max() / E32)
+    # most entries are far below the bound: a wrong or missing slab is not
+    assert float((err / size).mean()) < 4 * E32
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("normed", [False, True])
 def test_wgrad_single_products(dtype, normed):
