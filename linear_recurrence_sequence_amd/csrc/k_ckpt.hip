@@ -13,7 +13,7 @@ namespace msr {
 
 namespace {
 
-// A workgroup takes kFlat units of 8 values in a row, 256 at a time; four
+// Packing: a workgroup takes kFlat units of 8 values in a row, 256 at a time; four
 // neighbouring lanes hold a group of 32 (the number of units is a multiple
 // of 4, so a quad is on or off as one).  One short piece a workgroup, in
 // order: 32768 x 2560 bf16 packs in 40 us (6.3 TB/s) and reads back in 42; a
@@ -59,39 +59,116 @@ struct Norm8 {
   }
 };
 
-template <class T, int F, bool NORM>
-__global__ __launch_bounds__(256) void k_ckpt_unpack(CkptArgs a, T* __restrict__ X) {
-  const int cu = a.cols / 8;
-  const int64_t unit0 = (int64_t)blockIdx.x * kFlat, at = unit0 * 8;
-  const int n = (int)min((int64_t)kFlat, a.rows * cu - unit0);
-  const HeldWin<T, F> wq(a.q, a.qs, at, 8u * (uint32_t)n);
-  const Win wx(X + at, 8u * (uint32_t)n * (uint32_t)sizeof(T));
-  Held<T, F> h[kFlat / 256];
-#pragma unroll
-  for (int i = 0; i < kFlat / 256; ++i) h[i].load(wq, 8 * (threadIdx.x + 256 * i));
-  Norm8 nm[kFlat / 256];
-  float mu[kFlat / 256], r[kFlat / 256];
-  if constexpr (NORM) {
-    const Win ww(a.weight, 4u * (uint32_t)a.cols), wc(a.bias, 4u * (uint32_t)a.cols);
-    const int64_t row0 = unit0 / cu;                 // of the workgroup's first unit, and that unit's place in it
-    const uint32_t u0 = (uint32_t)(unit0 - row0 * cu), rows = (uint32_t)min((int64_t)(kFlat + 1), a.rows - row0);
-    const Win wm(a.mean ? a.mean + row0 : nullptr, 4u * rows), wr(a.rstd ? a.rstd + row0 : nullptr, 4u * rows);
-#pragma unroll
-    for (int i = 0; i < kFlat / 256; ++i) {
-      const uint32_t u = u0 + threadIdx.x + 256 * i, row = u / (uint32_t)cu;
-      nm[i].load(a, ww, wc, 8 * (u - row * (uint32_t)cu));
-      mu[i] = win_load_f32(wm, 4 * row);
-      r[i] = a.rstd ? win_load_f32(wr, 4 * row) : 1.f;
+// Reading back.  A thread's unit is 16 bytes of T: a wave stores whole lines
+// in one run (float32 as 8 values a thread, two stores of every other 16
+// bytes, and through the caches, took 64 us where this takes 57: 16384 x 4096).
+template <class T>
+constexpr int kUnit = 16 / (int)sizeof(T);
+
+template <class T, int F>
+struct Codes {
+  uint2 q;
+  uint32_t b;
+  // the unit at element offset `off`
+  __device__ __forceinline__ void load(const HeldWin<T, F>& w, uint32_t off) {
+    if constexpr (sizeof(T) == 2) {
+      const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(w.q.r, (int)off, 0, kStream);
+      q = make_uint2(v[0], v[1]);
+    } else {
+      q = make_uint2(__builtin_amdgcn_raw_buffer_load_b32(w.q.r, (int)off, 0, kStream), 0u);
     }
+    b = __builtin_amdgcn_raw_buffer_load_b8(w.qs.r, (int)(off >> 5), 0, 0);
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    float t[8];
+    q_decode8<F>(t, q);
+    const float s = q_pow2(b);
+#pragma unroll
+    for (int e = 0; e < kUnit<T>; ++e) v[e] = t[e] * s;
+  }
+};
+template <class T>
+__device__ __forceinline__ void store_unit(const Win& w, uint32_t off, const float* v) {
+  if constexpr (sizeof(T) == 2) {
+    Row8<bf16> o;
+    pack_row8(o, v);
+    win_store16(w, 2 * off, o.u);
+  } else {
+    win_store16(w, 4 * off, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                       __float_as_uint(v[3])));
+  }
+}
+
+template <class T, int F>
+__global__ __launch_bounds__(256) void k_ckpt_unpack(const uint8_t* __restrict__ q, const uint8_t* __restrict__ qs,
+                                                     T* __restrict__ X, int64_t count) {
+  constexpr int V = kUnit<T>, kTurns = kFlat / 256;
+  const int64_t at = (int64_t)blockIdx.x * kFlat * V;
+  const uint32_t n = (uint32_t)min((int64_t)kFlat * V, count - at);
+  const HeldWin<T, F> wq(q, qs, at, n);
+  const Win wx(X + at, n * (uint32_t)sizeof(T));
+  Codes<T, F> h[kTurns];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) h[i].load(wq, V * (threadIdx.x + 256 * i));
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    float v[V];
+    h[i].values(v);
+    store_unit<T>(wx, V * (threadIdx.x + 256 * i), v);
+  }
+}
+
+// Read back and normalised.  Weight and bias are 8 bytes for each byte of
+// codes, so a thread keeps its unit's for kNormRows turns.  A turn is a piece
+// of neighbouring units: `width` of a row (its units cut evenly into `pieces`
+// of at most 256), or, pieces 1, as many whole rows as 256 threads hold.
+// 16384 x 4096 with mean, rstd, weight and bias: bf16 38 us (62 with the
+// vectors read for each unit), float32 63 (105); 4 turns 40, 16 turns 41.
+constexpr int kNormRows = 8;
+
+template <class T, int F>
+__global__ __launch_bounds__(256) void k_ckpt_unpack_norm(CkptArgs a, T* __restrict__ X, int pieces, int width) {
+  constexpr int V = kUnit<T>;
+  const int cu = a.cols / V, tid = threadIdx.x;
+  const int piece = pieces == 1 ? 0 : (int)(blockIdx.x % (unsigned)pieces);
+  const int rpt = pieces == 1 ? (int)blockDim.x / cu : 1;          // rows a turn
+  const int64_t row0 = (int64_t)(blockIdx.x / (unsigned)pieces) * (rpt * kNormRows);
+  const int rib = pieces == 1 ? tid / cu : 0;                      // this thread's of them
+  const int c0 = piece * width;                                    // first unit of the piece
+  const uint32_t col = (uint32_t)(tid - rib * cu);
+  const int wide = V * min(width, cu - c0);
+  const int64_t x0 = V * (int64_t)c0;
+  const Win ww(a.weight ? a.weight + x0 : nullptr, 4u * (uint32_t)wide);
+  const Win wc(a.bias ? a.bias + x0 : nullptr, 4u * (uint32_t)wide);
+  f32x4 w[V / 4], c[V / 4];
+#pragma unroll
+  for (int k = 0; k < V / 4; ++k) {
+    w[k] = a.weight ? win_load_f32x4(ww, 4u * (V * col) + 16 * k) : (f32x4){1.f, 1.f, 1.f, 1.f};
+    c[k] = win_load_f32x4(wc, 4u * (V * col) + 16 * k);
+  }
+  Codes<T, F> h[kNormRows];
+  float mu[kNormRows], r[kNormRows];
+  // elements of turn i (rows past the end: none)
+  auto span = [&](int i) {
+    return (uint32_t)wide * (uint32_t)max((int64_t)0, min((int64_t)rpt, a.rows - row0 - i * rpt));
+  };
+  const uint32_t left = (uint32_t)min((int64_t)(rpt * kNormRows), a.rows - row0);
+  const Win wm(a.mean ? a.mean + row0 : nullptr, 4u * left), wr(a.rstd ? a.rstd + row0 : nullptr, 4u * left);
+#pragma unroll
+  for (int i = 0; i < kNormRows; ++i) {
+    h[i].load(HeldWin<T, F>(a.q, a.qs, (row0 + i * rpt) * a.cols + x0, span(i)), V * (uint32_t)tid);
+    mu[i] = win_load_f32(wm, 4u * (uint32_t)(i * rpt + rib));
+    r[i] = win_load_f32(wr, 4u * (uint32_t)(i * rpt + rib));
   }
 #pragma unroll
-  for (int i = 0; i < kFlat / 256; ++i) {
-    float v[8];
+  for (int i = 0; i < kNormRows; ++i) {
+    float v[V];
     h[i].values(v);
-    if constexpr (NORM) nm[i].apply(v, mu[i], r[i]);
-    Row8<T> o;
-    pack_row8(o, v);
-    win_store8(wx, 8 * (threadIdx.x + 256 * i), o);
+    const float ri = a.rstd ? r[i] : 1.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = (v[e] - mu[i]) * ri * w[e / 4][e % 4] + c[e / 4][e % 4];
+    const Win wx(X + (row0 + i * rpt) * a.cols + x0, span(i) * (uint32_t)sizeof(T));
+    store_unit<T>(wx, V * (uint32_t)tid, v);
   }
 }
 
@@ -299,10 +376,18 @@ hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipS
   const int64_t units = a.rows * a.cols / 8;
   if (units == 0) return hipSuccess;
   TraceScope ts("k_ckpt_unpack", st);
-  const dim3 g = flat_grid(units), b(256);
-#define MSR_UNPACK(T, F)                                                                               \
-  if (has_norm(a)) hipLaunchKernelGGL((k_ckpt_unpack<T, F, true>), g, b, 0, st, a, (T*)X);             \
-  else hipLaunchKernelGGL((k_ckpt_unpack<T, F, false>), g, b, 0, st, a, (T*)X);
+  const int V = elt == kBF16 ? kUnit<bf16> : kUnit<float>, cu = a.cols / V, quad = 32 / V;
+  int pieces = (cu + 255) / 256;
+  const int width = ((cu + pieces - 1) / pieces + quad - 1) / quad * quad;
+  pieces = (cu + width - 1) / width;
+  const int rpt = pieces == 1 ? 256 / cu : 1;
+  const int64_t per = has_norm(a) ? rpt * kNormRows : kFlat, n = has_norm(a) ? a.rows : a.rows * cu;
+  const int64_t blocks = (n + per - 1) / per * (has_norm(a) ? pieces : 1);
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 g((unsigned)blocks), bn((unsigned)(rpt * width));
+#define MSR_UNPACK(T, F)                                                                                         \
+  if (has_norm(a)) hipLaunchKernelGGL((k_ckpt_unpack_norm<T, F>), g, bn, 0, st, a, (T*)X, pieces, width);        \
+  else hipLaunchKernelGGL((k_ckpt_unpack<T, F>), g, dim3(256), 0, st, a.q, a.qs, (T*)X, a.rows * a.cols);
   if (elt == kBF16) {
     if (fmt == kQE4M3) { MSR_UNPACK(bf16, kQE4M3) } else { MSR_UNPACK(bf16, kQI8) }
   } else {

@@ -50,6 +50,10 @@ __device__ __forceinline__ void win_store16(const Win& w, uint32_t off, uint4 v)
 __device__ __forceinline__ float win_load_f32(const Win& w, uint32_t off) {
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(w.r, (int)off, 0, 0));
 }
+__device__ __forceinline__ f32x4 win_load_f32x4(const Win& w, uint32_t off) {
+  const uint4 u = win_load16<0>(w, off);
+  return (f32x4){__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+}
 __device__ __forceinline__ void win_store_f32(const Win& w, uint32_t off, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w.r, (int)off, 0, 0);
 }

@@ -166,6 +166,26 @@ def test_unpack_normalises(dtype):
             within("y", got, xh * w_ + c_, size * np.abs(w_) + np.abs(c_), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d", [(1, 32), (8, 96), (9, 1024), (17, 1056), (16, 2080), (65, 320), (1, 8192), (7, 33344)])
+def test_unpack_normalises_any_width(T, d, dtype):
+    """Widths that whole rows share a workgroup in, that are cut in equal and unequal pieces, and row counts about
+    those a workgroup takes; nothing is written beside the result."""
+    import torch
+    msr = _msr()
+    rng = np.random.default_rng(T + d)
+    q, qs, xv = keep(dev(normal(rng, (T, d), dtype, 2.0) + 1, dtype), "i8" if d % 64 else "e4m3")
+    mu, r = (v.astype(np.float32) for v in ot.norm_stats(xv, True, 1e-5))
+    w, c = (1 + 0.3 * rng.standard_normal(d)).astype(np.float32), rng.standard_normal(d).astype(np.float32)
+    say("unpack", dtype, T, d)
+    out, check = _guarded((T, d), torch_dtype(dtype))
+    got = msr.msr_ckpt_unpack(q, qs, mean=f32(mu), rstd=f32(r), weight=f32(w), bias=f32(c), out=out)
+    torch.cuda.synchronize()
+    xh, size = ot.normalised(xv, mu, r)
+    within("y", got, xh * w + c, size * np.abs(w) + np.abs(c), dtype)
+    check()
+
+
 # ------------------------------------------------------------- resid norm --
 SHAPES = [(1, 64), (5, 64), (67, 128), (2, 192), (33, 256), (7, 320), (9, 512), (70, 576), (5, 1024), (3, 2560),
           (13, 4096), (6, 4160), (3, 8192), (3001, 256), (1500, 1088)]
