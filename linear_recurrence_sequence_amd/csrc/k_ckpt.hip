@@ -13,11 +13,10 @@ namespace msr {
 
 namespace {
 
-// Packing: a workgroup takes kFlat units of 8 values in a row, 256 at a time; four
-// neighbouring lanes hold a group of 32 (the number of units is a multiple
-// of 4, so a quad is on or off as one).  One short piece a workgroup, in
-// order: 32768 x 2560 bf16 packs in 40 us (6.3 TB/s) and reads back in 42; a
-// grid of 2048 workgroups with strides took 46 each.
+// Packing: a workgroup takes kFlat units of 8 values in a row, 256 at a time.
+// One short piece a workgroup, in order: 32768 x 2560 bf16 packs in 40 us
+// (6.3 TB/s) and reads back in 42; a grid of 2048 workgroups with strides
+// took 46 each.
 constexpr int kFlat = 512;
 
 template <class T, int F>
@@ -29,12 +28,12 @@ __global__ __launch_bounds__(256) void k_ckpt_pack(const T* __restrict__ X, uint
   const HeldWin<T, F> wq(q, qs, at, 8u * (uint32_t)n);
   Row8<T> r[kFlat / 256];
 #pragma unroll
-  for (int i = 0; i < kFlat / 256; ++i) win_load8(r[i], wx, 8 * (threadIdx.x + 256 * i));
+  for (int i = 0; i < kFlat / 256; ++i) win_load8(r[i], wx, unit_of<T>(2048 * i, threadIdx.x, 256));
 #pragma unroll
   for (int i = 0; i < kFlat / 256; ++i) {
     float v[8];
     unpack_row8(v, r[i]);
-    q_store8(v, wq, 8 * (threadIdx.x + 256 * i));
+    q_store8(v, wq, unit_of<T>(2048 * i, threadIdx.x, 256));
   }
 }
 
@@ -44,14 +43,15 @@ struct Norm8 {
   float w[8], c[8];
   // the columns at element offset `col` of windows of weight and bias
   __device__ __forceinline__ void load(const CkptArgs& a, const Win& ww, const Win& wc, uint32_t col) {
-    Row8<float> rw, rc;
-    win_load8(rw, ww, col);
-    win_load8(rc, wc, col);
-    unpack_row8(w, rw);
-    unpack_row8(c, rc);
-    if (!a.weight)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = win_load_f32x4(ww, 4 * col + 16 * h), y = win_load_f32x4(wc, 4 * col + 16 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[4 * h + e] = a.weight ? x[e] : 1.f;
+        c[4 * h + e] = y[e];
+      }
+    }
   }
   __device__ __forceinline__ void apply(float* v, float mu, float r) const {
 #pragma unroll
@@ -255,13 +255,15 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
   const int c0 = blockIdx.y * 64;
   // the window of these rows (those past the end read as zeros)
   const uint32_t rows = (uint32_t)max((int64_t)0, min((int64_t)kTok, a.rows - t0));
-  const HeldWin<T, F> wq(a.q, a.qs, t0 * a.cols, rows * (uint32_t)a.cols);
+  // 8 neighbouring columns a thread, for either type
+  const HeldWin<bf16, F> wq(a.q, a.qs, t0 * a.cols, rows * (uint32_t)a.cols);
   const int c = tid & 7;
-  Held<T, F> h[kTok / 64][2];
+  Held<bf16, F> h[kTok / 64][2];
 #pragma unroll
   for (int i = 0; i < kTok / 64; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) h[i][j].load(wq, (uint32_t)((2 * (tid >> 3) + 64 * i + j) * a.cols + c0 + 8 * c));
+    for (int j = 0; j < 2; ++j)
+      h[i][j].load(wq, unit_of<bf16>((uint32_t)((2 * (tid >> 3) + 64 * i + j) * a.cols + c0), c, 8));
   float v[kTok / 64][2][8];
   if constexpr (NORM) {
     const Win ww(a.weight ? a.weight + c0 : nullptr, 256), wc(a.bias ? a.bias + c0 : nullptr, 256);

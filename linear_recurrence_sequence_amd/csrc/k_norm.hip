@@ -18,11 +18,11 @@
 //   dw = sum_t dn xh, dc = sum_t dn
 //
 // All of it streams: each tensor is read once and written once, bound by
-// HBM.  A lane holds 8 neighbouring values (16-byte loads of bf16); a row's
-// sums stay in registers and lane exchanges.  The sums over tokens (ds, dw,
-// dc) are carried in registers while a thread walks down its columns; the
-// walkers' float32 partials are then added in a fixed order in 64 bits by
-// k_col_sums (no atomics: the same bits every time).
+// HBM.  A lane holds 8 values (16-byte loads); a row's sums stay in registers
+// and lane exchanges.  The sums over tokens (ds, dw, dc) are carried in
+// registers while a thread walks down its columns; the walkers' float32
+// partials are then added in a fixed order in 64 bits by k_col_sums (no
+// atomics: the same bits every time).
 #include <algorithm>
 
 #include "msr_launch.h"
@@ -58,20 +58,6 @@ __device__ __forceinline__ void row_sums(float (&x)[NV], float (*red)[kMaxWaves]
     }
     turn ^= 1;
   }
-}
-
-__device__ __forceinline__ void load_vec8(float* v, const float* p, int64_t unit, bool ok, float def) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = def;
-  if (p && ok) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p + 8 * unit), b = *reinterpret_cast<const f32x4*>(p + 8 * unit + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-  }
-}
-__device__ __forceinline__ void store_vec8(float* p, const float* v) {
-  *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
-  *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
 }
 
 // alpha x + s b, each product and the sum rounded to float32 (no fused
@@ -120,8 +106,14 @@ struct RowMap {
     u0 = threadIdx.x - rib * tpr;
   }
   __device__ __forceinline__ int unit(int k) const { return u0 + k * tpr; }
-  __device__ __forceinline__ uint32_t off(int k) const {
-    return unit(k) < d / 8 ? (uint32_t)(rib * d + 8 * unit(k)) : kOutside;
+  // in its row, and behind the start of the workgroup's first row
+  template <class T>
+  __device__ __forceinline__ Unit at(int k) const {
+    return unit(k) < d / 8 ? unit_of<T>(0, unit(k), d / 8) : kNoUnit;
+  }
+  template <class T>
+  __device__ __forceinline__ Unit off(int k) const {
+    return unit(k) < d / 8 ? unit_of<T>((uint32_t)(rib * d), unit(k), d / 8) : kNoUnit;
   }
 };
 
@@ -137,15 +129,15 @@ __global__ __launch_bounds__(LPR ? 256 : 512) void k_resid_norm_fwd(ResidNormArg
   const RowMap<LPR> m(blockDim.x, a.d);
   const float inv_d = 1.f / (float)a.d;
   float w[VPT][8], c[VPT][8], s[VPT][8];
-  uint32_t off[VPT];
+  Unit off[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    off[k] = m.off(k);
-    const bool on = off[k] != kOutside;
-    load_vec8(w[k], a.weight, m.unit(k), on, 1.f);
-    load_vec8(c[k], a.bias, m.unit(k), on, 0.f);
+    off[k] = m.template off<T>(k);
+    const Unit at = m.template at<T>(k);
+    load_vec8(w[k], a.weight, at, 1.f);
+    load_vec8(c[k], a.bias, at, 0.f);
     // without B its window reads 0, and -1 * 0 = -0 changes no alpha x
-    load_vec8(s[k], a.scale, m.unit(k), on, a.B ? 1.f : -1.f);
+    load_vec8(s[k], a.scale, at, a.B ? 1.f : -1.f);
   }
   struct Row {
     Row8<T> x[VPT], b[VPT];
@@ -196,7 +188,7 @@ __global__ __launch_bounds__(LPR ? 256 : 512) void k_resid_norm_fwd(ResidNormArg
     float q[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const bool on = off[k] != kOutside;
+      const bool on = off[k].on();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         h[k][e] -= mu;
@@ -254,9 +246,10 @@ __global__ __launch_bounds__((bwd_threads<T, LPR, VPT>())) void k_resid_norm_bwd
   const float inv_d = 1.f / (float)a.d;
   f32x4* const vec = reinterpret_cast<f32x4*>(lds);             // [weight, scale][half][unit]
   for (int i = threadIdx.x; i < 4 * units; i += blockDim.x) {
-    const int v = i / (2 * units), j = i % (2 * units);          // vector, 16-byte piece
+    const int v = i / (2 * units), j = i % (2 * units);          // vector, 16-byte piece of it
+    const int half = sizeof(T) == 2 ? j & 1 : j >= units, u = sizeof(T) == 2 ? j >> 1 : j - half * units;
     const float* p = v ? a.scale : a.weight;
-    vec[v * 2 * kUnits + (j & 1) * kUnits + (j >> 1)] =
+    vec[v * 2 * kUnits + half * kUnits + u] =
         p ? *reinterpret_cast<const f32x4*>(p + 4 * j) : (f32x4){1.f, 1.f, 1.f, 1.f};
   }
   auto vec8 = [&](float* o, int v, int u) {
@@ -266,11 +259,11 @@ __global__ __launch_bounds__((bwd_threads<T, LPR, VPT>())) void k_resid_norm_bwd
   };
   __syncthreads();
   float aw[VPT][8], ac[VPT][8], as[DS ? VPT : 1][8];
-  uint32_t off[VPT];
+  Unit off[VPT];
   int unit[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    off[k] = m.off(k);
+    off[k] = m.template off<T>(k);
     unit[k] = min(m.unit(k), units - 1);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -361,14 +354,14 @@ __global__ __launch_bounds__((bwd_threads<T, LPR, VPT>())) void k_resid_norm_bwd
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       __syncthreads();
-      store_vec8(lds + 8 * threadIdx.x, v[k]);
+      store_vec8(lds, {8 * threadIdx.x, 8 * threadIdx.x + 4}, v[k]);
       __syncthreads();
-      if (m.rib == 0 && off[k] != kOutside) {
+      if (m.rib == 0 && off[k].on()) {
         float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int i = 0; i < m.rpb; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) t[e] += lds[8 * (i * m.tpr + m.u0) + e];
-        store_vec8(dst + (int64_t)blockIdx.x * a.d + 8 * m.unit(k), t);
+        store_vec8(dst + (int64_t)blockIdx.x * a.d, m.template at<T>(k), t);
       }
     }
   };
@@ -424,9 +417,19 @@ struct GateMap {
     col = (int)(i - (int64_t)t0 * units);
     on = t0 < R;
   }
-  // this thread's elements, and the bytes of its statistics, behind those of
-  // the first of the tokens that the grid holds side by side (R units <= 2^20)
-  __device__ __forceinline__ uint32_t off() const { return on ? 8u * (uint32_t)(t0 * units + col) : kOutside; }
+  // this thread's unit in a token
+  template <class T>
+  __device__ __forceinline__ Unit at(int lph) const {
+    return unit_of<T>(8u * (uint32_t)(col - col % lph), col % lph, lph);
+  }
+  // its unit, and the bytes of its statistics, behind those of the first of
+  // the tokens that the grid holds side by side (R units <= 2^20)
+  template <class T>
+  __device__ __forceinline__ Unit off(int lph) const {
+    const uint32_t t = 8u * (uint32_t)(t0 * units);
+    const Unit u = at<T>(lph);
+    return on ? Unit{t + u.lo, t + u.hi} : kNoUnit;
+  }
   __device__ __forceinline__ uint32_t stat_off(int heads, int lph) const {
     return on ? 4u * (uint32_t)(t0 * heads + col / lph) : kOutside;
   }
@@ -456,9 +459,10 @@ __global__ __launch_bounds__(256) void k_gated_norm_fwd(GatedNormArgs a) {
   const GateMap m(a.heads, LPH, a.R);
   constexpr float inv_d = 1.f / (8.f * LPH);
   float w[8], c[8];
-  load_vec8(w, a.weight, m.col, true, 1.f);
-  load_vec8(c, a.bias, m.col, true, 0.f);
-  const uint32_t off = m.off(), soff = m.col % LPH == 0 ? m.stat_off(a.heads, LPH) : kOutside;
+  const Unit off = m.template off<T>(LPH);
+  load_vec8(w, a.weight, m.template at<T>(LPH), 1.f);
+  load_vec8(c, a.bias, m.template at<T>(LPH), 0.f);
+  const uint32_t soff = m.col % LPH == 0 ? m.stat_off(a.heads, LPH) : kOutside;
   struct Row {
     Row8<T> o, g;
   };
@@ -513,8 +517,8 @@ __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
   float aw[8], ac[8];
   {
     float w[8], c[8];
-    load_vec8(w, a.weight, m.col, true, 1.f);
-    load_vec8(c, a.bias, m.col, true, 0.f);
+    load_vec8(w, a.weight, m.template at<T>(LPH), 1.f);
+    load_vec8(c, a.bias, m.template at<T>(LPH), 0.f);
     vec[0][threadIdx.x] = (f32x4){w[0], w[1], w[2], w[3]};
     vec[1][threadIdx.x] = (f32x4){w[4], w[5], w[6], w[7]};
     vec[2][threadIdx.x] = (f32x4){c[0], c[1], c[2], c[3]};
@@ -522,7 +526,8 @@ __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) aw[e] = ac[e] = 0.f;
-  const uint32_t off = m.off(), soff = m.stat_off(a.heads, LPH);
+  const Unit off = m.template off<T>(LPH);
+  const uint32_t soff = m.stat_off(a.heads, LPH);
   struct Row {
     Row8<T> z;
     Held<T, F> o, g;
@@ -583,21 +588,22 @@ __global__ __launch_bounds__(256) void k_gated_norm_bwd(GatedNormBwdArgs a) {
   const int64_t n = 8 * (int64_t)m.units;
   const bool whole = m.units <= 256;
   const int64_t P = whole ? (int64_t)gridDim.x : (int64_t)a.R;
-  float* dst = a.part + (whole ? (int64_t)blockIdx.x : (int64_t)m.t0) * n + 8 * m.col;
+  float* dst = a.part + (whole ? (int64_t)blockIdx.x : (int64_t)m.t0) * n;
+  const Unit at = m.template at<T>(LPH);
   auto put = [&](const float* v) {
     if (whole) {
       __syncthreads();
-      store_vec8(comb + 8 * threadIdx.x, v);
+      store_vec8(comb, {8 * threadIdx.x, 8 * threadIdx.x + 4}, v);
       __syncthreads();
       if ((int)threadIdx.x < m.units) {
         float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int i = threadIdx.x; i < (int)blockDim.x; i += m.units)
 #pragma unroll
           for (int e = 0; e < 8; ++e) t[e] += comb[8 * i + e];
-        store_vec8(dst, t);
+        store_vec8(dst, at, t);
       }
     } else if (m.on) {
-      store_vec8(dst, v);
+      store_vec8(dst, at, v);
     }
     dst += P * n;
   };

@@ -31,11 +31,9 @@ struct Win {
       : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, p ? (int)bytes : 0, 0x00027000)) {}
 };
 constexpr uint32_t kOutside = 0x7ffffff0u;     // beyond every window used
-// Cache policies.  bf16 and 8-bit tensors: non-temporal (gated norm backward
-// at 32768 x 16 x 512 from e4m3: 499 us, 514 with plain loads and stores;
-// packing 32768 x 2560: 42 us, 56 plain).  float32: plain -- a lane's 8
-// values are two 16-byte pieces, whose lines two instructions share (residual
-// norm at 16384 x 4096: forward 206 us, 229 non-temporal; backward 307, 329).
+// Cache policy of the tensors that are read or written once: non-temporal
+// (gated norm backward at 32768 x 16 x 512 from e4m3: 499 us, 514 with plain
+// loads and stores; packing 32768 x 2560 bf16: 42 us, 56 plain).
 constexpr int kStream = 2;
 
 template <int POLICY = kStream>
@@ -57,22 +55,53 @@ __device__ __forceinline__ f32x4 win_load_f32x4(const Win& w, uint32_t off) {
 __device__ __forceinline__ void win_store_f32(const Win& w, uint32_t off, float v) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), w.r, (int)off, 0, 0);
 }
-// 8 values at element offset `unit8` (a multiple of 8, or kOutside)
-__device__ __forceinline__ void win_load8(Row8<bf16>& r, const Win& w, uint32_t unit8) {
-  r.u = win_load16(w, unit8 == kOutside ? kOutside : 2 * unit8);
+// A lane's 8 values are two pieces of 4 neighbours, at element offsets lo and
+// hi (multiples of 4; lo = kOutside: neither).  bf16: next to each other, one
+// 16-byte access.  float32: hi a run of lanes further, so that neighbouring
+// lanes' pieces are neighbours in memory and each access covers whole lines
+// (16384 x 4096: residual norm forward 190 us, backward 135, gated norm
+// backward 228; with 8 neighbours a lane each access touched every other 16
+// bytes: 204, 150 and 252, and more non-temporal).
+// A group of 32 of the 8-bit form is 4 lanes' units or 8 lanes' pieces.
+struct Unit {
+  uint32_t lo, hi;
+  __device__ __forceinline__ bool on() const { return lo != kOutside; }
+};
+constexpr Unit kNoUnit = {kOutside, kOutside};
+// Lane l's unit of L lanes that hold 8 L neighbouring values from `base` on.
+template <class T>
+__device__ __forceinline__ Unit unit_of(uint32_t base, int l, int L) {
+  const uint32_t lo = base + (sizeof(T) == 2 ? 8u : 4u) * (uint32_t)l;
+  return {lo, lo + (sizeof(T) == 2 ? 4u : 4u * (uint32_t)L)};
 }
-__device__ __forceinline__ void win_load8(Row8<float>& r, const Win& w, uint32_t unit8) {
-  const uint32_t o = unit8 == kOutside ? kOutside : 4 * unit8;
-  r.lo = win_load16<0>(w, o);
-  r.hi = win_load16<0>(w, unit8 == kOutside ? kOutside : o + 16);
+__device__ __forceinline__ void win_load8(Row8<bf16>& r, const Win& w, Unit u) {
+  r.u = win_load16(w, u.on() ? 2 * u.lo : kOutside);
 }
-__device__ __forceinline__ void win_store8(const Win& w, uint32_t unit8, const Row8<bf16>& r) {
-  win_store16(w, unit8 == kOutside ? kOutside : 2 * unit8, r.u);
+__device__ __forceinline__ void win_load8(Row8<float>& r, const Win& w, Unit u) {
+  r.lo = win_load16(w, u.on() ? 4 * u.lo : kOutside);
+  r.hi = win_load16(w, u.on() ? 4 * u.hi : kOutside);
 }
-__device__ __forceinline__ void win_store8(const Win& w, uint32_t unit8, const Row8<float>& r) {
-  const uint32_t o = unit8 == kOutside ? kOutside : 4 * unit8;
-  win_store16<0>(w, o, r.lo);
-  win_store16<0>(w, unit8 == kOutside ? kOutside : o + 16, r.hi);
+__device__ __forceinline__ void win_store8(const Win& w, Unit u, const Row8<bf16>& r) {
+  win_store16(w, u.on() ? 2 * u.lo : kOutside, r.u);
+}
+__device__ __forceinline__ void win_store8(const Win& w, Unit u, const Row8<float>& r) {
+  win_store16(w, u.on() ? 4 * u.lo : kOutside, r.lo);
+  win_store16(w, u.on() ? 4 * u.hi : kOutside, r.hi);
+}
+// A float32 vector's 8 values (def where there is no vector or no unit), and
+// back.
+__device__ __forceinline__ void load_vec8(float* v, const float* p, Unit u, float def) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = def;
+  if (p && u.on()) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + u.lo), b = *reinterpret_cast<const f32x4*>(p + u.hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+  }
+}
+__device__ __forceinline__ void store_vec8(float* p, Unit u, const float* v) {
+  *reinterpret_cast<f32x4*>(p + u.lo) = (f32x4){v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + u.hi) = (f32x4){v[4], v[5], v[6], v[7]};
 }
 
 // Sum over aligned groups of L lanes (8, 16, 32 or 64), returned to all of
@@ -96,14 +125,17 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// Largest magnitude of the 4 lanes x 8 values of a group, as bits: magnitudes
-// compare as integers, infinities and NaN above every number.
-__device__ __forceinline__ uint32_t quad_amax(const float* v) {
+// Largest magnitude of a group, as bits: of N values of each of 32 / N lanes
+// (all of them active).  Magnitudes compare as integers, infinities and NaN
+// above every number.
+template <int N>
+__device__ __forceinline__ uint32_t group_amax(const float* v) {
   uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+  for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
   m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
   m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
+  if constexpr (N == 4) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));
   return m;
 }
 
@@ -124,25 +156,22 @@ __device__ __forceinline__ float q_pow2(uint32_t b) {
   return b == 255u ? __builtin_nanf("") : s;
 }
 
-// 8 values times `inv`, rounded to codes.
+// 4 values of a group with byte b as codes.  A group with an infinity or a
+// NaN reads back as NaN whatever its codes are: zeros.
 template <int F>
-__device__ __forceinline__ uint2 q_encode8(const float* v, float inv) {
-  uint2 r;
+__device__ __forceinline__ uint32_t q_encode4(const float* v, int b) {
+  const float inv = q_inv(b);
+  uint32_t r;
   if constexpr (F == kQE4M3) {
-    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
-    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
-    r.x = (uint32_t)lo;
-    r.y = (uint32_t)hi;
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+    r = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
   } else {
-    uint32_t b[8];
+    uint32_t c[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = (uint32_t)(int)rintf(v[e] * inv) & 0xffu;
-    r.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-    r.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+    for (int e = 0; e < 4; ++e) c[e] = (uint32_t)(int)rintf(v[e] * inv) & 0xffu;
+    r = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
   }
-  return r;
+  return b == 255 ? 0u : r;
 }
 
 // The numbers that 8 codes stand for, without their scale.
@@ -165,15 +194,6 @@ __device__ __forceinline__ void q_decode8(float* v, uint2 q) {
   }
 }
 
-// The 8-bit form of this lane's 8 values (its quad holds a whole group):
-// codes and the group's byte.  All four lanes of the quad have to be active.
-template <int F>
-__device__ __forceinline__ uint2 q_pack8(const float* v, int& b) {
-  b = q_scale<F>(quad_amax(v));
-  const uint2 c = q_encode8<F>(v, q_inv(b));
-  return b == 255 ? make_uint2(0u, 0u) : c;    // the group reads back as NaN whatever its codes are
-}
-
 // A tensor's window held in T (F = kQNone: the values) or in 8 bits (codes
 // and scale bytes): `rows` rows of d values from element `at` on.
 template <class T, int F>
@@ -188,41 +208,70 @@ struct HeldWin<T, kQNone> {
   __device__ __forceinline__ HeldWin(const void* x_, const uint8_t*, int64_t at, uint32_t n)
       : x(x_ ? (const T*)x_ + at : nullptr, n * (uint32_t)sizeof(T)) {}
 };
-// Packs 8 values at element offset `off` of the window.
+// Packs this lane's 8 values; the lanes of a group are active together.
 template <class T, int F>
-__device__ __forceinline__ void q_store8(const float* v, const HeldWin<T, F>& w, uint32_t off) {
-  int b;
-  const uint2 c = q_pack8<F>(v, b);
-  __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{c.x, c.y}, w.q.r, (int)off, 0, kStream);
-  const uint32_t so = (threadIdx.x & 3) == 0 ? off >> 5 : kOutside;
-  __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, w.qs.r, (int)so, 0, 0);
+__device__ __forceinline__ void q_store8(const float* v, const HeldWin<T, F>& w, Unit u) {
+  auto scale = [&](int b, uint32_t off, int lanes) {
+    const uint32_t so = u.on() && (threadIdx.x & (lanes - 1)) == 0 ? off >> 5 : kOutside;
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, w.qs.r, (int)so, 0, 0);
+  };
+  if constexpr (sizeof(T) == 2) {
+    const int b = q_scale<F>(group_amax<8>(v));
+    const u32x2_t c = {q_encode4<F>(v, b), q_encode4<F>(v + 4, b)};
+    __builtin_amdgcn_raw_buffer_store_b64(c, w.q.r, (int)u.lo, 0, kStream);
+    scale(b, u.lo, 4);
+  } else {
+    const int b0 = q_scale<F>(group_amax<4>(v)), b1 = q_scale<F>(group_amax<4>(v + 4));
+    __builtin_amdgcn_raw_buffer_store_b32(q_encode4<F>(v, b0), w.q.r, (int)u.lo, 0, kStream);
+    __builtin_amdgcn_raw_buffer_store_b32(q_encode4<F>(v + 4, b1), w.q.r, (int)u.hi, 0, kStream);
+    scale(b0, u.lo, 8);
+    scale(b1, u.hi, 8);
+  }
 }
 
-// 8 values of such a window, as loaded.  raw() gives them without their
-// scale, times scale() they are the values: what multiplies them anyway
-// takes it in.
+// 8 values of such a window, as loaded.  raw() times scale() are the values:
+// what multiplies them anyway takes the scale in (float32's pieces have one
+// each, raw() has taken them in).
 template <class T, int F>
 struct Held {
   uint2 q;
-  uint32_t b;
-  __device__ __forceinline__ void load(const HeldWin<T, F>& w, uint32_t off) {
-    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(w.q.r, (int)off, 0, kStream);
-    q = make_uint2(v[0], v[1]);
-    b = __builtin_amdgcn_raw_buffer_load_b8(w.qs.r, off == kOutside ? (int)kOutside : (int)(off >> 5), 0, 0);
+  uint32_t b, b1;
+  __device__ __forceinline__ void load(const HeldWin<T, F>& w, Unit u) {
+    auto scale = [&](uint32_t off) {
+      return __builtin_amdgcn_raw_buffer_load_b8(w.qs.r, u.on() ? (int)(off >> 5) : (int)kOutside, 0, 0);
+    };
+    if constexpr (sizeof(T) == 2) {
+      const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(w.q.r, (int)u.lo, 0, kStream);
+      q = make_uint2(v[0], v[1]);
+    } else {
+      q.x = __builtin_amdgcn_raw_buffer_load_b32(w.q.r, (int)u.lo, 0, kStream);
+      q.y = __builtin_amdgcn_raw_buffer_load_b32(w.q.r, (int)u.hi, 0, kStream);
+      b1 = scale(u.hi);
+    }
+    b = scale(u.lo);
   }
-  __device__ __forceinline__ float scale() const { return q_pow2(b); }
-  __device__ __forceinline__ void raw(float* v) const { q_decode8<F>(v, q); }
+  __device__ __forceinline__ float scale() const { return sizeof(T) == 2 ? q_pow2(b) : 1.f; }
+  __device__ __forceinline__ void raw(float* v) const {
+    q_decode8<F>(v, q);
+    if constexpr (sizeof(T) == 4) {
+      const float s = q_pow2(b), s1 = q_pow2(b1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { v[e] *= s; v[4 + e] *= s1; }
+    }
+  }
   __device__ __forceinline__ void values(float* v) const {
     raw(v);
-    const float s = scale();
+    if constexpr (sizeof(T) == 2) {
+      const float s = scale();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s;
+      for (int e = 0; e < 8; ++e) v[e] *= s;
+    }
   }
 };
 template <class T>
 struct Held<T, kQNone> {
   Row8<T> r;
-  __device__ __forceinline__ void load(const HeldWin<T, kQNone>& w, uint32_t off) { win_load8(r, w.x, off); }
+  __device__ __forceinline__ void load(const HeldWin<T, kQNone>& w, Unit u) { win_load8(r, w.x, u); }
   __device__ __forceinline__ float scale() const { return 1.f; }
   __device__ __forceinline__ void raw(float* v) const { unpack_row8(v, r); }
   __device__ __forceinline__ void values(float* v) const { unpack_row8(v, r); }
