@@ -595,6 +595,13 @@ class _On:
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
+    def like(self, x):
+        """An uninitialised tensor like x (contiguous), 1 us sooner than empty() has it."""
+        t = self.torch.empty_like(x)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
     def empty(self, shape, dtype):
         t = self.torch.empty(shape, dtype=dtype, device=self.device)
         if self.other is not None:
@@ -701,10 +708,10 @@ def msr_resid_norm_fwd(X, B=None, *, scale=None, weight=None, bias=None, alpha=1
     fmt, kept = _kept(dev, shape, ("H_q", H_q, H_qs), ("B_q", B_q, B_qs))
     with _On(X, stream) as on:
         if Y is None:
-            Y = on.empty(shape, ty)
+            Y = on.like(X)
             pY = Y.data_ptr()
         if H is None and not same:
-            H = on.empty(shape, ty)
+            H = on.like(X)
             pH = H.data_ptr()
         _check("msr_resid_norm_fwd",
                lib().msr_resid_norm_fwd(dt, norm, _rows_of(lead), d, alpha, eps, pX, pB, ps, pw, pc, pH, pY, pm, pr,
@@ -741,7 +748,7 @@ def msr_resid_norm_bwd(dY, H, mean, rstd, *, H_qs=None, dH=None, B=None, B_qs=No
     rows = _rows_of(lead)
     with _On(dY, stream) as on:
         if dX is None:
-            dX = on.empty(shape, ty)
+            dX = on.like(dY)
             pX = dX.data_ptr()
         need = 0 if pds is pdw is pdc is None else lib().msr_resid_norm_bwd_workspace_bytes(rows, d)
         ws, wsb, _keep = on.workspace(need, workspace)
@@ -768,7 +775,7 @@ def msr_gated_norm_fwd(O, G, *, weight=None, bias=None, norm=MSR_NORM_LAYER, eps
     fmt, kept = _kept(dev, shape, ("O_q", O_q, O_qs), ("G_q", G_q, G_qs))
     with _On(O, stream) as on:
         if Z is None:
-            Z = on.empty(shape, ty)
+            Z = on.like(O)
             pZ = Z.data_ptr()
         _check("msr_gated_norm_fwd",
                lib().msr_gated_norm_fwd(dt, norm, _rows_of(shape[:-2]), heads, dv, eps, pO, pG, pw, pc, pZ, pm, pr,
@@ -804,10 +811,10 @@ def msr_gated_norm_bwd(dZ, O, G, mean, rstd, *, O_qs=None, G_qs=None, weight=Non
     rows = _rows_of(shape[:-2])
     with _On(dZ, stream) as on:
         if dO is None:
-            dO = on.empty(shape, ty)
+            dO = on.like(dZ)
             pdO = dO.data_ptr()
         if dG is None:
-            dG = on.empty(shape, ty)
+            dG = on.like(dZ)
             pdG = dG.data_ptr()
         need = 0 if pdw is pdc is None else lib().msr_gated_norm_bwd_workspace_bytes(rows, heads, dv)
         ws, wsb, _keep = on.workspace(need, workspace)
