@@ -38,8 +38,20 @@ enum : int {
   kEpiRope = 1, kEpiGelu = 2, kEpiSigmoid = 4, kEpiBias = 8, kEpiResid = 16, kEpiPart = 32, kEpiAny = 63,
   // reduction range of a split product (with kEpiPart; GemmB::kextra, kvalid):
   // slices of K or K + 64, and of those one past the last row of B
-  kUneven = 64, kRagged = 128
+  kUneven = 64, kRagged = 128,
+  // slabs of 64 K rows are terms of a weight gradient's pieces
+  kTerms3 = 256, kTerms6 = 512
 };
+// The slab of the pieces of A (X) or B (dY) that reduction slab `slab` reads.
+template <int OPT>
+__device__ __forceinline__ int piece_slab(int slab, bool isA) {
+  if constexpr ((OPT & kTerms3) != 0) return isA ? (int)((unsigned)slab / 3u) : slab;
+  if constexpr ((OPT & kTerms6) != 0) {
+    const unsigned t = (unsigned)slab / 6u, j = (unsigned)slab - 6u * t;
+    return (int)(3u * t + ((isA ? 0x210100u : 0x012010u) >> (4u * j) & 3u));   // digit j: hi 0, mid 1, lo 2
+  }
+  return slab;
+}
 // First K row and K rows of slice z: K each, the first kextra slices 64 more.
 template <int OPT>
 __device__ __forceinline__ void split_range(const GemmB& bp, int K, int& kz, int& rows) {
@@ -457,7 +469,9 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
                                                                                                           : bp.ptr[3]);
   const int64_t ldb = sg0 == 0 ? bp.ld[0] : sg0 == 1 ? bp.ld[1] : sg0 == 2 ? bp.ld[2] : bp.ld[3];
   const int nb0 = n0 - (sg0 == 0 ? bp.start[0] : sg0 == 1 ? bp.start[1] : sg0 == 2 ? bp.start[2] : bp.start[3]);
-  const bf16* src = isA ? A + (size_t)m0 * lda + kz : bseg + nb0 + (size_t)kz * ldb;
+  constexpr bool TERMS = (EPI & (kTerms3 | kTerms6)) != 0;
+  const int kz0 = TERMS ? 0 : kz;
+  const bf16* src = isA ? A + (size_t)m0 * lda + kz0 : bseg + nb0 + (size_t)kz0 * ldb;
   const int64_t kstep = isA ? BK : BK * ldb;         // elements from one slab to the next
   uint32_t off[CPW];
 #pragma unroll
@@ -493,6 +507,10 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   auto issue = [&](int kt, int t) {
     const int kk = min(kt, KT - 1);
     const bf16* base = src + kk * kstep;
+    if constexpr (TERMS) {
+      const int k = kz + kk * BK;
+      base = src + (2 * piece_slab<EPI>(k / 64, isA) + (k / BK) % 2) * kstep;
+    }
     uint32_t o = off[t];
     if constexpr (RAG) {
       const bool tail = !isA && kz + kk * BK >= tail0;
@@ -643,8 +661,10 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
   auto sel = [&](auto a0, auto a1, auto a2, auto a3) { return sg == 0 ? a0 : (sg == 1 ? a1 : (sg == 2 ? a2 : a3)); };
   const bf16* Bs = reinterpret_cast<const bf16*>(sel(bp.ptr[0], bp.ptr[1], bp.ptr[2], bp.ptr[3]));
   const int64_t ldb = sel(bp.ld[0], bp.ld[1], bp.ld[2], bp.ld[3]);
-  const bf16* Bt = Bs + (n0 - sel(bp.start[0], bp.start[1], bp.start[2], bp.start[3])) + (size_t)kz * ldb;
-  const bf16* At = A + (size_t)m0 * lda + kz;
+  constexpr bool TERMS = (OPT & (kTerms3 | kTerms6)) != 0;
+  const int kz0 = TERMS ? 0 : kz;
+  const bf16* Bt = Bs + (n0 - sel(bp.start[0], bp.start[1], bp.start[2], bp.start[3])) + (size_t)kz0 * ldb;
+  const bf16* At = A + (size_t)m0 * lda + kz0;
 
   // Per-lane source offsets (elements) of this wave's copies; copy t fills
   // slots 64 (NW t + wave) + lane of the slab (A for t < ACP, then B).
@@ -675,8 +695,9 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
   auto issue = [&](int j) {
     const int jj = min(j, KT - 1);
     const uint32_t dst = (uint32_t)(uintptr_t)(lds + (j % NS) * STG) + wave * 1024;
-    const bf16* a = At + (size_t)jj * BK;
-    const bf16* b = Bt + (size_t)jj * BK * ldb;
+    const int js = TERMS ? kz / BK + jj : jj;
+    const bf16* a = At + (size_t)piece_slab<OPT>(js, true) * BK;
+    const bf16* b = Bt + (size_t)piece_slab<OPT>(js, false) * BK * ldb;
     // the slab that holds B's last row (the last one) reads the rows past it as that row (A holds zeros there)
     const bool tail = (OPT & kRagged) != 0 && kz + (jj + 1) * BK > bp.kvalid;
 #pragma unroll
@@ -912,10 +933,10 @@ hipError_t launch_gemm_splitk(Elt elt, const void* A, int64_t lda, const GemmB& 
 }
 
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int slabs, int rows, int splits, bool small_tiles, hipStream_t st) {
+                             int slabs, int rows, int terms, int splits, bool small_tiles, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
   if (N % 64 || (M + 127) / 128 > 65535 || splits < 1 || splits > slabs || rows <= 64 * (slabs - 1) ||
-      rows > 64 * slabs)
+      rows > 64 * slabs || (terms != 1 && ((terms != 3 && terms != 6) || slabs % terms || rows != 64 * slabs)))
     return hipErrorInvalidValue;
   GemmB b{};
   b.ptr[0] = B; b.ld[0] = ldb;
@@ -928,20 +949,30 @@ hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t 
   const bf16* a = (const bf16*)A;
   bf16* const none = nullptr;
   const dim3 block(512);
+  const bool ragged = rows < 64 * slabs;
+  const int64_t ldc = N;
+#define MSR_BY_TERMS(LAUNCH)                                 \
+  if (terms == 6) { LAUNCH(kUneven | kTerms6) }              \
+  else if (terms == 3) { LAUNCH(kUneven | kTerms3) }         \
+  else if (ragged) { LAUNCH(kUneven | kRagged) }             \
+  else { LAUNCH(kUneven) }
   if (small_tiles) {
     const dim3 grid(N / 64, (M + 127) / 128, splits);
-    if (rows < 64 * slabs)
-      hipLaunchKernelGGL((k_gemm_sk<true, kUneven | kRagged>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
-    else
-      hipLaunchKernelGGL((k_gemm_sk<true, kUneven>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
+#define MSR_PARTS(OPT) \
+  hipLaunchKernelGGL((k_gemm_sk<true, OPT>), grid, block, 0, st, a, lda, b, none, ldc, M, N, K);
+    MSR_BY_TERMS(MSR_PARTS)
+#undef MSR_PARTS
     return hipGetLastError();
   }
   const dim3 grid((N + 255) / 256, (M + 255) / 256, splits);
-#define MSR_PARTS(OPT)                                                                                              \
-  if (N <= 8192) hipLaunchKernelGGL((k_gemm_dc<OPT, 4, 8, 1>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K); \
-  else hipLaunchKernelGGL((k_gemm_dc<OPT, 4, 8, 0>), grid, block, 0, st, a, lda, b, none, (int64_t)N, M, N, K);
-  if (rows < 64 * slabs) { MSR_PARTS(kEpiPart | kUneven | kRagged) } else { MSR_PARTS(kEpiPart | kUneven) }
+#define MSR_PARTS(OPT)                                                                                      \
+  if (N <= 8192)                                                                                            \
+    hipLaunchKernelGGL((k_gemm_dc<kEpiPart | OPT, 4, 8, 1>), grid, block, 0, st, a, lda, b, none, ldc, M, N, K); \
+  else                                                                                                      \
+    hipLaunchKernelGGL((k_gemm_dc<kEpiPart | OPT, 4, 8, 0>), grid, block, 0, st, a, lda, b, none, ldc, M, N, K);
+  MSR_BY_TERMS(MSR_PARTS)
 #undef MSR_PARTS
+#undef MSR_BY_TERMS
   return hipGetLastError();
 }
 

@@ -281,20 +281,24 @@ struct CkptArgs {
   const float* mean; const float* rstd; const float* weight; const float* bias;
 };
 hipError_t launch_ckpt_unpack(Elt elt, int fmt, const CkptArgs& a, void* X, hipStream_t st);
-// Operands of a weight gradient X^T dY as bf16 terms (see k_ckpt.hip): terms
-// 1 (bf16 tensors), 3 (float32) or 6 (float32, normalised X).  Token t's term
-// j stands at reduction index ((t / 64) terms + j) 64 + t % 64; indexes past
-// the last token, up to ld = the tokens rounded up to 64, times terms, hold
-// zeros.
-// XT[col][index] bf16, row stride ld; a.cols a multiple of 64.
+// A weight gradient X^T dY as a sum of products of bf16 pieces (see
+// k_ckpt.hip): terms 1 (bf16 tensors), 3 (float32) or 6 (float32, normalised
+// X) of X's and dY's pieces.
+struct WgradPieces {
+  int x, dy;
+};
+constexpr WgradPieces wgrad_pieces(int terms) { return {terms == 6 ? 3 : 1, terms == 1 ? 1 : 3}; }
+// Its operands, of P pieces each: token t's piece p stands at index ((t / 64)
+// P + p) 64 + t % 64; tokens past the last, up to 64 slabs, hold zeros.
+// XT[col][index] bf16; a.cols a multiple of 64.
 struct WgradOperands {
   CkptArgs a;
   uint16_t* XT;
-  int64_t ld;
-  const float* dY;                   // terms > 1: [rows, dy_cols], cut into terms; dy_cols a multiple of 8
+  int64_t slabs;                     // of 64 tokens
+  const float* dY;                   // terms > 1: [rows, dy_cols], cut into pieces; dy_cols a multiple of 8
   int64_t dy_rows;
   int dy_cols;
-  uint16_t* dYt;                     // [ld, dy_cols] bf16
+  uint16_t* dYt;                     // [index][dy_cols] bf16
 };
 hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperands& w, hipStream_t st);
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
@@ -305,7 +309,11 @@ hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n,
 // has `rows` rows, 64 (slabs - 1) < rows <= 64 slabs; A's columns past them
 // hold zeros (what is read as B's rows there is its last one).  N a
 // multiple of 64; on 256 x 256 tiles, or small_tiles: 128 x 64.
+// terms 3 or 6: `slabs` counts terms, A and B are a weight gradient's
+// operands in pieces, rows = 64 slabs; terms of a token slab follow each
+// other: 3: X with hi, mid, lo of dY; 6: hi hi, hi mid, mid hi, hi lo, mid
+// mid, lo hi.
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int slabs, int rows, int splits, bool small_tiles, hipStream_t st);
+                             int slabs, int rows, int terms, int splits, bool small_tiles, hipStream_t st);
 
 }  // namespace msr

@@ -264,8 +264,10 @@ WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int
     }
   }
   size_t off = 0;
-  w.xt = off; off += up256((size_t)d_in * w.slabs * 64 * 2);
-  w.dyt = off; off += dtype == MSR_F32 ? up256((size_t)w.slabs * 64 * d_out * 2) : 0;
+  const WgradPieces p = wgrad_pieces(terms);
+  const size_t tokens = (size_t)(w.slabs / terms) * 64;
+  w.xt = off; off += up256((size_t)d_in * tokens * p.x * 2);
+  w.dyt = off; off += dtype == MSR_F32 ? up256(tokens * p.dy * d_out * 2) : 0;
   w.part = off; off += w.splits > 1 || accumulate ? up256((size_t)w.splits * d_in * d_out * sizeof(float)) : 0;
   w.total = off;
   return w;
@@ -281,7 +283,7 @@ msr_status check_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d_in
     return fail(MSR_ERR_SHAPE, "invalid sizes rows=%d d_in=%d d_out=%d", rows, d_in, d_out);
   if (d_in % 64 || d_out % 64 || d_in > (1 << 20) || d_out > (1 << 20))
     return fail(MSR_ERR_UNSUPPORTED, "d_in = %d and d_out = %d must be multiples of 64 up to 2^20", d_in, d_out);
-  // a tile's 256 rows of X^T (six terms a token) have 32-bit byte offsets
+  // a tile's 256 rows of X^T (three pieces a token) have 32-bit byte offsets
   if (rows > (1 << 20)) return fail(MSR_ERR_UNSUPPORTED, "rows = %d exceeds 2^20", rows);
   return MSR_OK;
 }
@@ -315,12 +317,13 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
   const bool f32 = dtype == MSR_F32;
   float* part = w.splits > 1 || accumulate ? (float*)(ws + w.part) : dW;
   const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)(ws + w.xt),
-                          w.slabs * 64, f32 ? (const float*)dY : nullptr, rows, d_out,
+                          w.slabs / terms, f32 ? (const float*)dY : nullptr, rows, d_out,
                           f32 ? (uint16_t*)(ws + w.dyt) : nullptr};
   hipError_t err = launch_wgrad_operands(elt_of(dtype), (int)fmt, terms, ops, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(operands)");
-  err = launch_gemm_parts(ws + w.xt, w.slabs * 64, f32 ? (const void*)(ws + w.dyt) : dY, d_out, part, d_in, d_out,
-                          (int)w.slabs, f32 ? (int)w.slabs * 64 : rows, w.splits, w.small, st);
+  const int64_t ld = w.slabs / terms * wgrad_pieces(terms).x * 64;
+  err = launch_gemm_parts(ws + w.xt, ld, f32 ? (const void*)(ws + w.dyt) : dY, d_out, part, d_in, d_out,
+                          (int)w.slabs, f32 ? (int)w.slabs * 64 : rows, terms, w.splits, w.small, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
   if (part != dW) err = launch_sum_parts(part, w.splits, dW, n, accumulate != 0, st);
   return from_hip(err, "msr_ckpt_wgrad(sum)");
