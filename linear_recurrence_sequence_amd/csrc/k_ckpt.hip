@@ -203,7 +203,7 @@ __device__ __forceinline__ void cut3(float x, float (&p)[3]) {
 // pair as one 32-bit word; then each column's tokens leave as 128-byte lines.
 // A tile row of kTok + 8 tokens is 4 banks (mod 64) longer than the last, so
 // that a wave's writes (8 columns apart, two tokens apart) spread over the
-// banks.  The workgroups behind the last columns write the terms of dY.
+// banks.  The workgroups behind the last columns write dY's part.
 constexpr int kTok = 128;
 
 template <class T, int F, bool NORM, int TERMS>
@@ -213,16 +213,21 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
   const CkptArgs& a = w.a;
   const int tid = threadIdx.x;
   if ((int)blockIdx.y >= a.cols / 64) {
-    // one unit of 8 columns of a token (with those padded) at a time
-    if constexpr (TERMS > 1) {
-      const int cu = w.dy_cols / 8;
-      const int64_t units = 64 * w.slabs * cu, step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
-      for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + tid; u < units;
-           u += step) {
-        const int64_t row = u / cu;
-        const bool in = row < w.dy_rows;
-        Row8<float> r;
-        load_row8(r, w.dY + 8 * (in ? u : 0), in);
+    // one unit of 8 columns of a token (with those padded) at a time, of all
+    // (float32) or of the last slab's
+    const int cu = w.dy_cols / 8;
+    const int64_t slab0 = TERMS == 1 ? w.slabs - 1 : 0;
+    const int64_t units = 64 * (w.slabs - slab0) * cu, step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
+    const T* const src = (const T*)w.dY + 64 * slab0 * w.dy_cols;
+    for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + tid; u < units;
+         u += step) {
+      const int64_t row = u / cu;
+      const bool in = 64 * slab0 + row < w.dy_rows;
+      Row8<T> r;
+      load_row8(r, src + 8 * (in ? u : 0), in);
+      if constexpr (TERMS == 1) {
+        store_row8((bf16*)w.dYt + 8 * u, r);
+      } else {
         float v[8], p[3][8];
         unpack_row8(v, r);
 #pragma unroll
@@ -393,7 +398,7 @@ hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperand
   const CkptArgs& a = w.a;
   if (a.cols == 0 || w.slabs == 0) return hipSuccess;
   const int64_t tokens = 64 * w.slabs, gx = (tokens + kTok - 1) / kTok;
-  const int64_t dy_units = terms > 1 ? tokens * (w.dy_cols / 8) : 0;
+  const int64_t dy_units = w.dYt ? (terms > 1 ? tokens : 64) * (w.dy_cols / 8) : 0;
   const int64_t gy = a.cols / 64 + std::min<int64_t>(((dy_units + 255) / 256 + gx - 1) / gx, 4096);
   if (a.cols % 64 || w.dy_cols % 8 || gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
   TraceScope ts("k_wgrad_operands", st);

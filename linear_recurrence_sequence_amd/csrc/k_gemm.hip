@@ -36,9 +36,9 @@ namespace msr {
 // time and serves any combination).
 enum : int {
   kEpiRope = 1, kEpiGelu = 2, kEpiSigmoid = 4, kEpiBias = 8, kEpiResid = 16, kEpiPart = 32, kEpiAny = 63,
-  // reduction range of a split product (with kEpiPart; GemmB::kextra, kvalid):
-  // slices of K or K + 64, and of those one past the last row of B
-  kUneven = 64, kRagged = 128,
+  // reduction range of a split product (with kEpiPart; GemmB::kextra, tail):
+  // slices of K or K + 64, and the last rows of B elsewhere
+  kUneven = 64, kTail = 128,
   // slabs of 64 K rows are terms of a weight gradient's pieces
   kTerms3 = 256, kTerms6 = 512
 };
@@ -490,20 +490,10 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   // copy t of slab kt into its ring slot; slabs past the end copy the last
   // slab again (into a slot no slab still needs), so that every step issues
   // the same copies and the waits are fixed
-  // Ragged: the slab that holds B's last row reads the rows past it as that
-  // row, and so does a slab behind it, from that slab again (A holds zeros
-  // there).  Selected without a branch, so that the copies stay between the
-  // MFMAs.
-  constexpr bool RAG = (EPI & kRagged) != 0;
-  const int tail0 = RAG ? (bp.kvalid - 1) / BK * BK : 0;   // first row of that slab
-  uint32_t toff[RAG ? CPW : 1];
-  if constexpr (RAG) {
-#pragma unroll
-    for (int t = 0; t < CPW; ++t) {
-      const int kr = (((wave % (NW / 2)) * CPW + t) * 64 + lane) >> 5;
-      toff[t] = off[t] - (uint32_t)((kr - min(kr, bp.kvalid - 1 - tail0)) * ldb * 2);
-    }
-  }
+  // B's rows from tail0 on are another matrix's: selected without a branch,
+  // so that the copies stay between the MFMAs.
+  constexpr bool TAIL = (EPI & kTail) != 0;
+  const bf16* const tsrc = TAIL && !isA ? reinterpret_cast<const bf16*>(bp.tail) + nb0 : nullptr;
   auto issue = [&](int kt, int t) {
     const int kk = min(kt, KT - 1);
     const bf16* base = src + kk * kstep;
@@ -511,13 +501,11 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
       const int k = kz + kk * BK;
       base = src + (2 * piece_slab<EPI>(k / 64, isA) + (k / BK) % 2) * kstep;
     }
-    uint32_t o = off[t];
-    if constexpr (RAG) {
-      const bool tail = !isA && kz + kk * BK >= tail0;
-      base = tail ? src + (tail0 - kz) * ldb : base;
-      o = tail ? toff[t] : o;
+    if constexpr (TAIL) {
+      const int past = kz + kk * BK - bp.tail0;
+      base = !isA && past >= 0 ? tsrc + past * ldb : base;
     }
-    copy16_to_lds(base, o, lbase + (uint32_t)((kt % NS) * SLOTS * 16 + t * 1024));
+    copy16_to_lds(base, off[t], lbase + (uint32_t)((kt % NS) * SLOTS * 16 + t * 1024));
   };
 
   // Fragments: lane lr reads row lr of a 32-row block, chunk 2 s + hh of
@@ -680,14 +668,6 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
       off[t] = (uint32_t)(r * ldb + 8 * c);
     }
   }
-  uint32_t toff[(OPT & kRagged) != 0 ? CPW - ACP : 1];
-  if constexpr ((OPT & kRagged) != 0) {
-#pragma unroll
-    for (int t = ACP; t < CPW; ++t) {
-      const int r = (64 * (NW * t + wave) + lane - ASL) / CPR;
-      toff[t - ACP] = off[t] - (uint32_t)((r - min(r, (bp.kvalid - 1) % BK)) * ldb);
-    }
-  }
   lds_char* const lds = (lds_char*)smem;
   // copies of slab j into its slot (slabs past the last re-copy the last
   // one, into a slot no wave reads again, so that every slab issues CPW
@@ -698,15 +678,11 @@ __global__ __launch_bounds__(512) void k_gemm_sk(const bf16* __restrict__ A, int
     const int js = TERMS ? kz / BK + jj : jj;
     const bf16* a = At + (size_t)piece_slab<OPT>(js, true) * BK;
     const bf16* b = Bt + (size_t)piece_slab<OPT>(js, false) * BK * ldb;
-    // the slab that holds B's last row (the last one) reads the rows past it as that row (A holds zeros there)
-    const bool tail = (OPT & kRagged) != 0 && kz + (jj + 1) * BK > bp.kvalid;
+    if constexpr ((OPT & kTail) != 0)                // B's last slab stands elsewhere
+      b = kz + jj * BK >= bp.tail0 ? reinterpret_cast<const bf16*>(bp.tail) + n0 : b;
 #pragma unroll
-    for (int t = 0; t < CPW; ++t) {
-      uint32_t o = off[t];
-      if constexpr ((OPT & kRagged) != 0)
-        if (t >= ACP) o = tail ? toff[t - ACP] : o;
-      copy16_to_lds(t < ACP ? a : b, 2 * o, __builtin_amdgcn_readfirstlane(dst + t * NW * 1024));
-    }
+    for (int t = 0; t < CPW; ++t)
+      copy16_to_lds(t < ACP ? a : b, 2 * off[t], __builtin_amdgcn_readfirstlane(dst + t * NW * 1024));
   };
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) issue(j);
@@ -933,28 +909,28 @@ hipError_t launch_gemm_splitk(Elt elt, const void* A, int64_t lda, const GemmB& 
 }
 
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int slabs, int rows, int terms, int splits, bool small_tiles, hipStream_t st) {
+                             int slabs, const void* tail, int terms, int splits, bool small_tiles, hipStream_t st) {
   if (M == 0 || N == 0) return hipSuccess;
-  if (N % 64 || (M + 127) / 128 > 65535 || splits < 1 || splits > slabs || rows <= 64 * (slabs - 1) ||
-      rows > 64 * slabs || (terms != 1 && ((terms != 3 && terms != 6) || slabs % terms || rows != 64 * slabs)))
+  if (N % 64 || (M + 127) / 128 > 65535 || splits < 1 || splits > slabs ||
+      (terms != 1 && ((terms != 3 && terms != 6) || slabs % terms || tail)))
     return hipErrorInvalidValue;
   GemmB b{};
   b.ptr[0] = B; b.ld[0] = ldb;
   b.start[0] = 0; b.start[1] = b.start[2] = b.start[3] = INT32_MAX;
   b.part = part;
   b.kextra = slabs % splits;
-  b.kvalid = rows;
+  b.tail0 = 64 * (slabs - 1);
+  b.tail = tail;
   const int K = slabs / splits * 64;
   TraceScope ts("k_gemm", st);
   const bf16* a = (const bf16*)A;
   bf16* const none = nullptr;
   const dim3 block(512);
-  const bool ragged = rows < 64 * slabs;
   const int64_t ldc = N;
 #define MSR_BY_TERMS(LAUNCH)                                 \
   if (terms == 6) { LAUNCH(kUneven | kTerms6) }              \
   else if (terms == 3) { LAUNCH(kUneven | kTerms3) }         \
-  else if (ragged) { LAUNCH(kUneven | kRagged) }             \
+  else if (tail) { LAUNCH(kUneven | kTail) }                 \
   else { LAUNCH(kUneven) }
   if (small_tiles) {
     const dim3 grid(N / 64, (M + 127) / 128, splits);

@@ -161,9 +161,10 @@ struct GemmB {
   // [z K_s, (z + 1) K_s) and stores float32 partials to part + z M N (no
   // rotation); launch_gemm_splitk adds them up.
   float* part;
-  // launch_gemm_parts: the first kextra slices take 64 more K rows, and B has
-  // kvalid rows
-  int kextra, kvalid;
+  // launch_gemm_parts: the first kextra slices take 64 more K rows; the K
+  // rows from tail0 on are those of `tail` (row stride ld[0])
+  int kextra, tail0;
+  const void* tail;
   // epilogue: C = act(A B + bias) + resid, act = gelu when act == 1 and
   // sigmoid when act == 2 (after any rotation), bias[s] a float32 vector
   // over segment s's columns (nullable), resid an [M, N] matrix with row
@@ -295,25 +296,26 @@ struct WgradOperands {
   CkptArgs a;
   uint16_t* XT;
   int64_t slabs;                     // of 64 tokens
-  const float* dY;                   // terms > 1: [rows, dy_cols], cut into pieces; dy_cols a multiple of 8
+  // dY [dy_rows, dy_cols] (dy_cols a multiple of 8).  float32: its pieces in
+  // dYt[index][dy_cols].  bf16: the product reads it in place, but for a last
+  // slab that it does not fill: with zeros behind it in dYt [64, dy_cols].
+  const void* dY;
   int64_t dy_rows;
   int dy_cols;
-  uint16_t* dYt;                     // [index][dy_cols] bf16
+  uint16_t* dYt;
 };
 hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperands& w, hipStream_t st);
 // out[i] = (accumulate ? out[i] : 0) + sum over z < parts of part[z n + i], n a multiple of 4.
 hipError_t launch_sum_parts(const float* part, int parts, float* out, int64_t n, bool accumulate, hipStream_t st);
 // float32 products of K slices of bf16 matrices: the 64 slabs rows of K are
 // cut into `splits` slices of whole slabs (the first slabs % splits one slab
-// longer), slice z's product of A[m][k] B[k][n] in part[z M N + m N + n].  B
-// has `rows` rows, 64 (slabs - 1) < rows <= 64 slabs; A's columns past them
-// hold zeros (what is read as B's rows there is its last one).  N a
+// longer), slice z's product of A[m][k] B[k][n] in part[z M N + m N + n].  The
+// last slab's rows of B are `tail` (row stride ldb) where that is given.  N a
 // multiple of 64; on 256 x 256 tiles, or small_tiles: 128 x 64.
-// terms 3 or 6: `slabs` counts terms, A and B are a weight gradient's
-// operands in pieces, rows = 64 slabs; terms of a token slab follow each
-// other: 3: X with hi, mid, lo of dY; 6: hi hi, hi mid, mid hi, hi lo, mid
-// mid, lo hi.
+// terms 3 or 6 (no tail): `slabs` counts terms, A and B are a weight
+// gradient's operands in pieces; terms of a token slab follow each other: 3:
+// X with hi, mid, lo of dY; 6: hi hi, hi mid, mid hi, hi lo, mid mid, lo hi.
 hipError_t launch_gemm_parts(const void* A, int64_t lda, const void* B, int64_t ldb, float* part, int M, int N,
-                             int slabs, int rows, int terms, int splits, bool small_tiles, hipStream_t st);
+                             int slabs, const void* tail, int terms, int splits, bool small_tiles, hipStream_t st);
 
 }  // namespace msr

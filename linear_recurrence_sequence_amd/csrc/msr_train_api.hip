@@ -224,8 +224,10 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
 
 }  // extern "C"
 
-// Weight gradient: the operands as bf16 terms in the workspace (X^T always,
-// dY where it is float32; a bf16 dY is read in place), then the product over
+// Weight gradient: the operands as bf16 pieces in the workspace (X^T always,
+// dY where it is float32; a bf16 dY is read in place, but for a last slab
+// that it does not fill: the product reads a copy with zeros behind it, whose
+// rows meet zeros of X that would make an infinity a NaN), the product over
 // the reduction indexes (tokens times terms), 64 of them a slab, in `splits`
 // slices of whole slabs.  Each slice gives a float32 partial; a single one is
 // dW itself.
@@ -267,7 +269,8 @@ WgradPlan wgrad_plan(msr_dtype dtype, int terms, int32_t rows, int32_t d_in, int
   const WgradPieces p = wgrad_pieces(terms);
   const size_t tokens = (size_t)(w.slabs / terms) * 64;
   w.xt = off; off += up256((size_t)d_in * tokens * p.x * 2);
-  w.dyt = off; off += dtype == MSR_F32 ? up256(tokens * p.dy * d_out * 2) : 0;
+  const size_t dy_rows = dtype == MSR_F32 ? tokens * p.dy : rows % 64 ? 64 : 0;
+  w.dyt = off; off += up256(dy_rows * d_out * 2);
   w.part = off; off += w.splits > 1 || accumulate ? up256((size_t)w.splits * d_in * d_out * sizeof(float)) : 0;
   w.total = off;
   return w;
@@ -316,14 +319,14 @@ msr_status msr_ckpt_wgrad(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t d
   char* ws = (char*)workspace;
   const bool f32 = dtype == MSR_F32;
   float* part = w.splits > 1 || accumulate ? (float*)(ws + w.part) : dW;
-  const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)(ws + w.xt),
-                          w.slabs / terms, f32 ? (const float*)dY : nullptr, rows, d_out,
-                          f32 ? (uint16_t*)(ws + w.dyt) : nullptr};
+  uint16_t* dyt = f32 || rows % 64 ? (uint16_t*)(ws + w.dyt) : nullptr;
+  const int64_t slabs = w.slabs / terms;
+  const WgradOperands ops{{rows, d_in, (const uint8_t*)q, qs, mean, rstd, weight, bias}, (uint16_t*)(ws + w.xt), slabs,
+                          dY, rows, d_out, dyt};
   hipError_t err = launch_wgrad_operands(elt_of(dtype), (int)fmt, terms, ops, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(operands)");
-  const int64_t ld = w.slabs / terms * wgrad_pieces(terms).x * 64;
-  err = launch_gemm_parts(ws + w.xt, ld, f32 ? (const void*)(ws + w.dyt) : dY, d_out, part, d_in, d_out,
-                          (int)w.slabs, f32 ? (int)w.slabs * 64 : rows, terms, w.splits, w.small, st);
+  err = launch_gemm_parts(ws + w.xt, slabs * wgrad_pieces(terms).x * 64, f32 ? dyt : dY, d_out, part, d_in, d_out,
+                          (int)w.slabs, f32 ? nullptr : dyt, terms, w.splits, w.small, st);
   if (err != hipSuccess) return from_hip(err, "msr_ckpt_wgrad(product)");
   if (part != dW) err = launch_sum_parts(part, w.splits, dW, n, accumulate != 0, st);
   return from_hip(err, "msr_ckpt_wgrad(sum)");

@@ -430,6 +430,28 @@ def test_wgrad_keeps_bad_values_in_their_row_and_column(dtype):
 
 # ----------------------------------------------------- limits and isolation --
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,i,o", [(65, 64, 128), (77, 64, 128), (100, 320, 192), (1000, 2048, 2048), (16383, 512, 8192)])
+def test_wgrad_last_token_infinite(T, i, o, dtype):
+    """An infinity in the last token's gradient gives infinities of its products' signs, however many tokens lie
+    beside it in the last block of a reduction."""
+    import torch
+    msr = _msr()
+    say("wgrad, last token infinite", dtype, T, i, o)
+    gen = torch.Generator().manual_seed(T)
+    x = torch.randn(T, i, generator=gen).cuda()
+    x[-1] = torch.where(torch.arange(i, device="cuda") % 3 == 0, -2.0, 1.0)
+    dY = torch.randn(T, o, generator=gen).cuda().to(torch_dtype(dtype))
+    dY[-1, 5], dY[-1, 70] = float("inf"), float("-inf")
+    q, qs = msr.msr_ckpt_pack(x)
+    dW = msr.msr_ckpt_wgrad(q, qs, dY)
+    sign = torch.sign(msr.msr_ckpt_unpack(q, qs, torch.float32)[-1])
+    assert torch.equal(dW[:, 5], sign * float("inf")) and torch.equal(dW[:, 70], sign * float("-inf"))
+    rest = torch.ones(o, dtype=torch.bool, device="cuda")
+    rest[[5, 70]] = False
+    assert bool(dW[:, rest].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_no_tokens(dtype):
     """No rows: nothing read, the sums over tokens are zero, an accumulated gradient stays."""
     import torch
