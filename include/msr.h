@@ -417,9 +417,9 @@ msr_status msr_ckpt_unpack(msr_dtype dtype, msr_qfmt fmt, int32_t rows, int32_t 
  *   dW = X^T dY  (accumulate != 0: dW += X^T dY),  float32 [d_in, d_out],
  * X [rows, d_in] read back and normalised as in msr_ckpt_unpack and, where it
  * is normalised, rounded to dtype; dY: [rows, d_out] (dtype).  Products are
- * exact (float32 dtype, normalised: to 2^-25 of each; magnitudes below 2^-126
- * count as zero there; an infinity in dY may come out as a NaN in its column
- * there), added in float32.
+ * exact and added in float32; in float32 dtype the values of X and dY are
+ * taken to 2^-133 (bf16's smallest) and, X normalised, products to 2^-25 of
+ * each, and an infinity in dY may come out as a NaN in its column then.
  * d_in and d_out multiples of 64, at most 2^20; rows at most 2^20.
  * Workspace: msr_ckpt_wgrad_workspace_bytes(), normed != 0 where any of mean,
  * rstd, weight, bias is given. */

@@ -429,6 +429,24 @@ def test_wgrad_keeps_bad_values_in_their_row_and_column(dtype):
 
 
 # ----------------------------------------------------- limits and isolation --
+@pytest.mark.parametrize("normed", [False, True])
+def test_wgrad_of_tiny_gradients(normed):
+    """float32 gradients down to its smallest: each is taken to 2^-133 (X is 1; normalised, to 2^-25 of it as well)."""
+    import torch
+    msr = _msr()
+    T = 64
+    e, m = np.meshgrid(np.arange(-149, -85), 1 + 2.0 ** -np.arange(1.0, 24.0))
+    v = np.resize((m * 2.0 ** e).ravel(), (64 * 23,)).astype(np.float32)
+    say("wgrad of tiny gradients", normed)
+    q, qs = msr.msr_ckpt_pack(torch.ones(T, 64, device="cuda"))
+    kw = dict(rstd=torch.ones(T, device="cuda")) if normed else {}
+    dW = host(msr.msr_ckpt_wgrad(q, qs, torch.from_numpy(v).cuda().expand(T, -1).contiguous(), **kw))
+    want = T * v.astype(np.float64)
+    # T products of one sign: each sum rounds by half a unit of at most its end
+    tol = T * 2.0 ** -133 + want * (T * E32 + (2.0 ** -25 if normed else 0))
+    assert np.all(np.abs(dW - want) <= tol), np.max(np.abs(dW - want) / tol)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,i,o", [(65, 64, 128), (77, 64, 128), (100, 320, 192), (1000, 2048, 2048), (16383, 512, 8192)])
 def test_wgrad_last_token_infinite(T, i, o, dtype):
