@@ -181,10 +181,10 @@ __global__ __launch_bounds__(256) void k_ckpt_unpack_norm(CkptArgs a, T* __restr
 // normalised X is three bf16 as well, and of the nine products the six down
 // to 2^-16 are taken (the others are below 2^-26 of the value).  The bf16
 // units are 16 times as fast as the float32 ones: 16384 x 2560 x 4096 took
-// 1030 us against 4250 us on the latter.
+// 1005 us against 4250 us on the latter.
 // Each piece is written once, 64 tokens of it a slab; the product picks the
 // pieces that meet (written once a term instead, X normalised: 2054 us for
-// 1908, and 1434 MB of workspace for 780; 192 x 4096: 421 for 336).
+// 1908, and 1434 MB of workspace for 780).
 
 // x cut into three bf16 (as floats) that add up to it: each takes the leading
 // 8 bits of what is left (toward zero: nothing overflows).  Infinities and
@@ -205,6 +205,10 @@ __device__ __forceinline__ void cut3(float x, float (&p)[3]) {
 // that a wave's writes (8 columns apart, two tokens apart) spread over the
 // banks.  The workgroups behind the last columns write dY's part.
 constexpr int kTok = 128;
+// Quads of 4 columns of dY a workgroup cuts, each lane a 16-byte load, all in
+// flight: 16384 x 4096 takes 100 us, 6.7 TB/s (8 columns a lane, one load at a
+// time down a strided grid: 150; the pieces stored non-temporally: 119).
+constexpr int kDy = 1024;
 
 template <class T, int F, bool NORM, int TERMS>
 __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
@@ -213,36 +217,47 @@ __global__ __launch_bounds__(256) void k_wgrad_operands(WgradOperands w) {
   const CkptArgs& a = w.a;
   const int tid = threadIdx.x;
   if ((int)blockIdx.y >= a.cols / 64) {
-    // one unit of 8 columns of a token (with those padded) at a time, of all
-    // (float32) or of the last slab's
-    const int cu = w.dy_cols / 8;
-    const int64_t slab0 = TERMS == 1 ? w.slabs - 1 : 0;
-    const int64_t units = 64 * (w.slabs - slab0) * cu, step = (int64_t)(gridDim.y - a.cols / 64) * gridDim.x * 256;
-    const T* const src = (const T*)w.dY + 64 * slab0 * w.dy_cols;
-    for (int64_t u = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * 256 + tid; u < units;
-         u += step) {
-      const int64_t row = u / cu;
-      const bool in = 64 * slab0 + row < w.dy_rows;
-      Row8<T> r;
-      load_row8(r, src + 8 * (in ? u : 0), in);
+    // kDy quads of 4 neighbouring columns a workgroup, of all tokens (float32)
+    // or of the last slab's, those padded among them: read as zeros
+    const int cu = w.dy_cols / 4;
+    const int64_t slab0 = TERMS == 1 ? w.slabs - 1 : 0, first = 64 * slab0 * cu;
+    const int64_t q0 = ((int64_t)(blockIdx.y - a.cols / 64) * gridDim.x + blockIdx.x) * kDy;
+    const int64_t quads = 64 * (w.slabs - slab0) * cu;
+    if (q0 >= quads) return;
+    const int64_t left = max((int64_t)0, w.dy_rows * cu - first - q0);
+    const Win wy((const T*)w.dY + 4 * (first + q0), (uint32_t)min(left, (int64_t)kDy) * 4u * (uint32_t)sizeof(T));
+    const int64_t row0 = q0 / cu;
+    const uint32_t u0 = (uint32_t)(q0 - row0 * cu), n = (uint32_t)min(quads - q0, (int64_t)kDy);
+    uint4 r[kDy / 256];
+#pragma unroll
+    for (int i = 0; i < kDy / 256; ++i) {
+      const uint32_t u = tid + 256 * i;
       if constexpr (TERMS == 1) {
-        store_row8((bf16*)w.dYt + 8 * u, r);
+        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(wy.r, (int)(8 * u), 0, 0);
+        r[i] = make_uint4(v[0], v[1], 0u, 0u);
       } else {
-        float v[8], p[3][8];
-        unpack_row8(v, r);
+        r[i] = win_load16(wy, 16 * u);
+      }
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float q[3];
-          cut3(v[e], q);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) p[i][e] = q[i];
-        }
-        bf16* const dst = (bf16*)w.dYt + (row / 64 * (64 * 3) + row % 64) * w.dy_cols + 8 * (u - row * cu);
+    for (int i = 0; i < kDy / 256; ++i) {
+      const uint32_t u = tid + 256 * i;
+      if (u >= n) break;
+      if constexpr (TERMS == 1) {
+        *reinterpret_cast<uint2*>(w.dYt + 4 * (q0 + u)) = make_uint2(r[i].x, r[i].y);
+      } else {
+        const uint32_t dr = (u0 + u) / (uint32_t)cu, row = (uint32_t)row0 + dr;
+        const uint32_t col = u0 + u - dr * (uint32_t)cu;
+        uint16_t* const dst = w.dYt + ((int64_t)(row / 64 * (64 * 3) + row % 64) * cu + col) * 4;
+        float p[4][3];
+        cut3(__uint_as_float(r[i].x), p[0]);
+        cut3(__uint_as_float(r[i].y), p[1]);
+        cut3(__uint_as_float(r[i].z), p[2]);
+        cut3(__uint_as_float(r[i].w), p[3]);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-          Row8<bf16> o;
-          pack_row8(o, p[j]);
-          store_row8(dst + (int64_t)(64 * j) * w.dy_cols, o);
+          const u32x2_t v = {pack_bf16(p[0][j], p[1][j]), pack_bf16(p[2][j], p[3][j])};
+          *reinterpret_cast<u32x2_t*>(dst + (int64_t)(64 * j) * w.dy_cols) = v;
         }
       }
     }
@@ -398,8 +413,8 @@ hipError_t launch_wgrad_operands(Elt elt, int fmt, int terms, const WgradOperand
   const CkptArgs& a = w.a;
   if (a.cols == 0 || w.slabs == 0) return hipSuccess;
   const int64_t tokens = 64 * w.slabs, gx = (tokens + kTok - 1) / kTok;
-  const int64_t dy_units = w.dYt ? (terms > 1 ? tokens : 64) * (w.dy_cols / 8) : 0;
-  const int64_t gy = a.cols / 64 + std::min<int64_t>(((dy_units + 255) / 256 + gx - 1) / gx, 4096);
+  const int64_t dy_wgs = w.dYt ? ((terms > 1 ? tokens : 64) * (w.dy_cols / 4) + kDy - 1) / kDy : 0;
+  const int64_t gy = a.cols / 64 + (dy_wgs + gx - 1) / gx;
   if (a.cols % 64 || w.dy_cols % 8 || gx > INT32_MAX || gy > 65535) return hipErrorInvalidValue;
   TraceScope ts("k_wgrad_operands", st);
   const dim3 g((unsigned)gx, (unsigned)gy), b(256);
