@@ -493,17 +493,15 @@ __global__ __launch_bounds__(64 * NW) void k_gemm_dc(const bf16* __restrict__ A,
   // B's rows from tail0 on are another matrix's: selected without a branch,
   // so that the copies stay between the MFMAs.
   constexpr bool TAIL = (EPI & kTail) != 0;
-  const bf16* const tsrc = TAIL && !isA ? reinterpret_cast<const bf16*>(bp.tail) + nb0 : nullptr;
+  // (tsrc stands where slab 0 of that matrix would be).
+  const int ktail = TAIL && !isA ? (bp.tail0 - kz) / BK : INT32_MAX;
+  const bf16* const tsrc = TAIL && !isA ? reinterpret_cast<const bf16*>(bp.tail) + nb0 - ktail * kstep : src;
   auto issue = [&](int kt, int t) {
     const int kk = min(kt, KT - 1);
-    const bf16* base = src + kk * kstep;
+    const bf16* base = (TAIL && kk >= ktail ? tsrc : src) + kk * kstep;
     if constexpr (TERMS) {
       const int k = kz + kk * BK;
       base = src + (2 * piece_slab<EPI>(k / 64, isA) + (k / BK) % 2) * kstep;
-    }
-    if constexpr (TAIL) {
-      const int past = kz + kk * BK - bp.tail0;
-      base = !isA && past >= 0 ? tsrc + past * ldb : base;
     }
     copy16_to_lds(base, off[t], lbase + (uint32_t)((kt % NS) * SLOTS * 16 + t * 1024));
   };
